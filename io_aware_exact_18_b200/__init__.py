@@ -84,6 +84,12 @@ def load_library(path: str = LIB_PATH):
     lib.fa_last_device_error.restype = i
     lib.fa_watchdog_selftest.argtypes = [ctypes.c_uint64, vp]
     lib.fa_watchdog_selftest.restype = i
+    lib.fa_qk_rotary.argtypes = [ctypes.c_char_p, vp]
+    lib.fa_qk_rotary.restype = i
+    lib.fa_qk_rotary_bwd.argtypes = [ctypes.c_char_p, vp, sz, vp]
+    lib.fa_qk_rotary_bwd.restype = i
+    lib.fa_qk_rotary_bwd_workspace_bytes.argtypes = [i, i, i, i, i, i]
+    lib.fa_qk_rotary_bwd_workspace_bytes.restype = sz
     if path == LIB_PATH:
         _lib = lib
     return lib
@@ -385,3 +391,6 @@ def decode_attention_fp8(q8, k8, v8, q_descale, k_descale, v_descale, scale=None
     if check and st != FA_OK:
         raise FAError(st, "fa_fwd_splitkv_fp8")
     return out, lse
+
+
+from .rotary import qk_rotary, qk_rotary_bwd, rotary_frequencies  # noqa: E402

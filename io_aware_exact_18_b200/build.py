@@ -12,9 +12,10 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libfa.so")
-SOURCES = [os.path.join(CSRC, "fa_api.cu")]
-HEADERS = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + [
-    os.path.join(ROOT, "include", "fa.h")]
+SOURCES = [os.path.join(CSRC, f) for f in ("fa_api.cu", "fa_rotary.cu")]
+INCLUDE = os.path.join(ROOT, "include")
+HEADERS = [os.path.join(d, f) for d in (CSRC, INCLUDE) for f in os.listdir(d)
+           if f.endswith((".cuh", ".h"))]
 
 NVCC_FLAGS = [
     "-O3", "-std=c++17",
@@ -24,6 +25,7 @@ NVCC_FLAGS = [
     "-Xptxas", "-v",
     "--expt-relaxed-constexpr",
     "-shared",
+    "--threads", "0",      # the sources side by side
 ]
 
 
@@ -42,7 +44,7 @@ def up_to_date() -> bool:
 def build(force: bool = False, verbose: bool = False) -> str:
     if not force and up_to_date():
         return LIB
-    cmd = [nvcc(), *NVCC_FLAGS, "-I", os.path.join(ROOT, "include"), "-I", CSRC,
+    cmd = [nvcc(), *NVCC_FLAGS, "-I", INCLUDE, "-I", CSRC,
            *SOURCES, "-o", LIB + ".tmp", "-lcuda"]
     res = subprocess.run(cmd, capture_output=True, text=True)
     log = os.path.join(PKG, "build.log")

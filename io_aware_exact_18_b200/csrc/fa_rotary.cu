@@ -1,0 +1,226 @@
+// Host side of fa_rotary.h: argument checks and launches.
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "fa_host.h"
+#include "fa_rotary_launch.h"
+
+namespace fa {
+
+int rotary_check(const fa_rotary_t& r, int d) {
+    if (d != 64 && d != 128 && d != 256) return FA_ERR_UNSUPPORTED;
+    if (r.rotary_dim < 0 || r.rotary_dim > d || r.rotary_dim % 16 != 0) return FA_ERR_INVALID_ARG;
+    if ((r.interleaved | 1) != 1 || (r.norm | 1) != 1 || (r.weight_f32 | 1) != 1)
+        return FA_ERR_INVALID_ARG;
+    if (!std::isfinite(r.rotary_scale)) return FA_ERR_INVALID_ARG;
+    if (r.norm && (!std::isfinite(r.norm_eps) || r.norm_eps < 0.f)) return FA_ERR_INVALID_ARG;
+    const uintptr_t wmask = r.weight_f32 ? 3u : 1u;
+    if (r.norm && ((addr(r.q_weight) | addr(r.k_weight)) & wmask) != 0) return FA_ERR_INVALID_ARG;
+    if (r.rotary_dim > 0 && (r.freqs == nullptr || (addr(r.freqs) & 7u) != 0))
+        return FA_ERR_INVALID_ARG;
+    return FA_OK;
+}
+
+namespace {
+
+// B, H, H_kv, N within what the kernels index: every product fits 63 bits and
+// the grid 31.
+int sizes_check(int B, int H, int H_kv, int N) {
+    if (B < 0 || H < 0 || H_kv < 0 || N < 0) return FA_ERR_INVALID_ARG;
+    if ((int64_t)B * N > INT32_MAX || H > 65536 || H_kv > 65536) return FA_ERR_INVALID_ARG;
+    return FA_OK;
+}
+
+// Every view usable, every output with rows of its own, apart from the inputs
+// (or exactly the one it may replace) and from the other outputs.
+int views_check(const View* in, int n_in, const View* out, int n_out, const int* replaces) {
+    for (int i = 0; i < n_in; ++i)
+        if (in[i].H != 0 && !view_ok(in[i])) return FA_ERR_INVALID_ARG;
+    for (int o = 0; o < n_out; ++o) {
+        if (out[o].H == 0) continue;
+        if (!view_ok(out[o]) || !rows_distinct(out[o])) return FA_ERR_INVALID_ARG;
+        for (int i = 0; i < n_in; ++i) {
+            if (in[i].H == 0 || (i == replaces[o] && same_view(in[i], out[o]))) continue;
+            if (!views_apart(in[i], out[o])) return FA_ERR_INVALID_ARG;
+        }
+        for (int u = 0; u < o; ++u)
+            if (out[u].H != 0 && !views_apart(out[u], out[o])) return FA_ERR_INVALID_ARG;
+    }
+    return FA_OK;
+}
+
+template <int D, bool kNorm, bool kInter>
+void launch_fwd_d(RotParams p, cudaStream_t s) {
+    const int64_t blocks = rot_tiling(&p, RotCfg<D>::kSlots, p.H + p.H_kv);
+    fa_qk_rotary_fwd<D, kNorm, kInter, kDense><<<(unsigned)blocks, kRotThreads, 0, s>>>(p);
+}
+
+template <int D>
+void launch_fwd(const RotParams& p, bool norm, bool inter, cudaStream_t s) {
+    if (norm) inter ? launch_fwd_d<D, true, true>(p, s) : launch_fwd_d<D, true, false>(p, s);
+    else inter ? launch_fwd_d<D, false, true>(p, s) : launch_fwd_d<D, false, false>(p, s);
+}
+
+int launch_fwd_any(const RotParams& p, int d, bool norm, bool inter, cudaStream_t s) {
+    if (d == 64) launch_fwd<64>(p, norm, inter, s);
+    else if (d == 128) launch_fwd<128>(p, norm, inter, s);
+    else launch_fwd<256>(p, norm, inter, s);
+    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+int fwd(const fa_qk_rotary_t& a, void* stream) {
+    int rc = rotary_check(a.rotary, a.d);
+    if (rc == FA_OK) rc = sizes_check(a.B, a.H, a.H_kv, a.N);
+    if (rc != FA_OK) return rc;
+    if (a.B == 0 || a.N == 0 || a.H + a.H_kv == 0) return FA_OK;
+    if (a.rotary.rotary_dim > 0 &&
+        !positions_ok(a.positions, a.pos_stride_b, a.pos_stride_n, a.B, a.N))
+        return FA_ERR_INVALID_ARG;
+    const View in[2] = {{a.q, a.B, a.H, a.N, a.d}, {a.k, a.B, a.H_kv, a.N, a.d}};
+    const View out[2] = {{a.q_out, a.B, a.H, a.N, a.d}, {a.k_out, a.B, a.H_kv, a.N, a.d}};
+    const int replaces[2] = {0, 1};
+    rc = views_check(in, 2, out, 2, replaces);
+    if (rc != FA_OK) return rc;
+    int dev = 0;
+    rc = device_ready(&dev);
+    if (rc != FA_OK) return rc;
+    RotParams p{};
+    p.q = rot_rows(a.q);
+    p.k = rot_rows(a.k);
+    p.qo = rot_rows(a.q_out);
+    p.ko = rot_rows(a.k_out);
+    rot_fill(&p, a.rotary, a.positions, a.pos_stride_b, a.pos_stride_n, a.B, a.H, a.H_kv, a.N);
+    return launch_fwd_any(p, a.d, a.rotary.norm, a.rotary.interleaved,
+                          static_cast<cudaStream_t>(stream));
+}
+
+int slots_of(int d) { return d == 64 ? RotCfg<64>::kSlots : d == 128 ? RotCfg<128>::kSlots
+                                                                     : RotCfg<256>::kSlots; }
+
+// Blocks of the backward with the norm: its items, up to kRotBwdBlocks.
+int64_t bwd_blocks(int B, int H, int H_kv, int N, int d, int64_t* items) {
+    RotParams p{};
+    p.tokens = (int64_t)B * N;
+    *items = rot_tiling(&p, slots_of(d), H + H_kv);
+    return std::min<int64_t>(*items, kRotBwdBlocks);
+}
+
+template <int D>
+int launch_bwd(RotBwdParams bp, bool inter, float* dwq, float* dwk, cudaStream_t s) {
+    bp.items = rot_tiling(&bp.f, RotCfg<D>::kSlots, bp.f.H + bp.f.H_kv);
+    const int blocks = (int)std::min<int64_t>(bp.items, kRotBwdBlocks);
+    if (inter) fa_qk_rotary_bwd_norm<D, true><<<blocks, kRotThreads, 0, s>>>(bp);
+    else fa_qk_rotary_bwd_norm<D, false><<<blocks, kRotThreads, 0, s>>>(bp);
+    if (cudaGetLastError() != cudaSuccess) return FA_ERR_LAUNCH;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(2 * D / 32);
+    cfg.blockDim = dim3(32, 32);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e =
+        cudaLaunchKernelEx(&cfg, fa_rotary_dw<D>, (const float*)bp.part, blocks, dwq, dwk);
+    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
+int bwd(const fa_qk_rotary_bwd_t& a, void* ws, size_t ws_bytes, void* stream) {
+    int rc = rotary_check(a.rotary, a.d);
+    if (rc == FA_OK) rc = sizes_check(a.B, a.H, a.H_kv, a.N);
+    if (rc != FA_OK) return rc;
+    const bool norm = a.rotary.norm != 0;
+    if (norm && (!a.dq_weight || !a.dk_weight ||
+                 ((addr(a.dq_weight) | addr(a.dk_weight)) & 3u) != 0 ||
+                 bytes_meet(a.dq_weight, 4 * a.d, a.dk_weight, 4 * a.d)))
+        return FA_ERR_INVALID_ARG;
+    if (!norm && (a.dq_weight || a.dk_weight)) return FA_ERR_INVALID_ARG;
+    const bool empty = a.B == 0 || a.N == 0 || a.H + a.H_kv == 0;
+    if (empty && !norm) return FA_OK;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int dev = 0;
+    if (empty) {                      // no rows: the weights' gradients are zero
+        rc = device_ready(&dev);
+        if (rc != FA_OK) return rc;
+        return cudaMemsetAsync(a.dq_weight, 0, 4 * a.d, s) == cudaSuccess &&
+                       cudaMemsetAsync(a.dk_weight, 0, 4 * a.d, s) == cudaSuccess
+                   ? FA_OK
+                   : FA_ERR_LAUNCH;
+    }
+    if (a.rotary.rotary_dim > 0 &&
+        !positions_ok(a.positions, a.pos_stride_b, a.pos_stride_n, a.B, a.N))
+        return FA_ERR_INVALID_ARG;
+    const View in[4] = {{a.dq_out, a.B, a.H, a.N, a.d}, {a.dk_out, a.B, a.H_kv, a.N, a.d},
+                        {a.q, a.B, a.H, a.N, a.d}, {a.k, a.B, a.H_kv, a.N, a.d}};
+    const View out[2] = {{a.dq, a.B, a.H, a.N, a.d}, {a.dk, a.B, a.H_kv, a.N, a.d}};
+    const int replaces[2] = {0, 1};
+    rc = views_check(in, norm ? 4 : 2, out, 2, replaces);
+    if (rc != FA_OK) return rc;
+    int64_t items = 0;
+    const size_t need =
+        norm ? (size_t)bwd_blocks(a.B, a.H, a.H_kv, a.N, a.d, &items) * 2 * a.d * 4 : 0;
+    if (norm) {
+        if (ws == nullptr || (addr(ws) & 15u) != 0 || ws_bytes < need) return FA_ERR_INVALID_ARG;
+        struct Buf { const void* p; size_t n; };
+        const Buf w[3] = {{ws, need}, {a.dq_weight, 4 * (size_t)a.d}, {a.dk_weight, 4 * (size_t)a.d}};
+        for (int i = 0; i < 3; ++i) {
+            for (const View& v : in)
+                if (bytes_meet(w[i].p, w[i].n, v.t.ptr, view_bytes(v))) return FA_ERR_INVALID_ARG;
+            for (const View& v : out)
+                if (bytes_meet(w[i].p, w[i].n, v.t.ptr, view_bytes(v))) return FA_ERR_INVALID_ARG;
+            if (i > 0 && bytes_meet(ws, need, w[i].p, w[i].n)) return FA_ERR_INVALID_ARG;
+        }
+    }
+    rc = device_ready(&dev);
+    if (rc != FA_OK) return rc;
+    RotParams p{};
+    rot_fill(&p, a.rotary, a.positions, a.pos_stride_b, a.pos_stride_n, a.B, a.H, a.H_kv, a.N);
+    p.sin_sign = -1.f;                // the transpose of a rotation turns back
+    p.qo = rot_rows(a.dq);
+    p.ko = rot_rows(a.dk);
+    if (!norm) {                      // dx = g: the forward with the angles negated
+        p.q = rot_rows(a.dq_out);
+        p.k = rot_rows(a.dk_out);
+        return launch_fwd_any(p, a.d, false, a.rotary.interleaved, s);
+    }
+    p.q = rot_rows(a.q);
+    p.k = rot_rows(a.k);
+    RotBwdParams bp{};
+    bp.f = p;
+    bp.dq_out = rot_rows(a.dq_out);
+    bp.dk_out = rot_rows(a.dk_out);
+    bp.part = static_cast<float*>(ws);
+    const bool inter = a.rotary.interleaved != 0;
+    if (a.d == 64) return launch_bwd<64>(bp, inter, a.dq_weight, a.dk_weight, s);
+    if (a.d == 128) return launch_bwd<128>(bp, inter, a.dq_weight, a.dk_weight, s);
+    return launch_bwd<256>(bp, inter, a.dq_weight, a.dk_weight, s);
+}
+
+}  // namespace
+}  // namespace fa
+
+#define FA_EXPORT __attribute__((visibility("default")))
+
+extern "C" {
+
+FA_EXPORT int fa_qk_rotary(const fa_qk_rotary_t* args, void* stream) {
+    return args == nullptr ? FA_ERR_INVALID_ARG : fa::fwd(*args, stream);
+}
+
+FA_EXPORT int fa_qk_rotary_bwd(const fa_qk_rotary_bwd_t* args, void* workspace,
+                               size_t workspace_bytes, void* stream) {
+    return args == nullptr ? FA_ERR_INVALID_ARG
+                           : fa::bwd(*args, workspace, workspace_bytes, stream);
+}
+
+FA_EXPORT size_t fa_qk_rotary_bwd_workspace_bytes(int B, int H, int H_kv, int N, int d, int norm) {
+    if ((d != 64 && d != 128 && d != 256) || fa::sizes_check(B, H, H_kv, N) != FA_OK || !norm ||
+        B == 0 || N == 0 || H + H_kv == 0)
+        return 0;
+    int64_t items = 0;
+    return (size_t)fa::bwd_blocks(B, H, H_kv, N, d, &items) * 2 * (size_t)d * 4;
+}
+
+}  // extern "C"
