@@ -90,6 +90,14 @@ def load_library(path: str = LIB_PATH):
     lib.fa_qk_rotary_bwd.restype = i
     lib.fa_qk_rotary_bwd_workspace_bytes.argtypes = [i, i, i, i, i, i]
     lib.fa_qk_rotary_bwd_workspace_bytes.restype = sz
+    lib.fa_paged_append.argtypes = [ctypes.c_char_p, vp]
+    lib.fa_paged_append.restype = i
+    lib.fa_paged_decode.argtypes = [ctypes.c_char_p, vp, sz, vp]
+    lib.fa_paged_decode.restype = i
+    lib.fa_paged_decode_workspace_bytes.argtypes = [i, i, i, i]
+    lib.fa_paged_decode_workspace_bytes.restype = sz
+    lib.fa_copy_pages.argtypes = [ctypes.c_char_p, vp, vp, i, vp]
+    lib.fa_copy_pages.restype = i
     if path == LIB_PATH:
         _lib = lib
     return lib
@@ -393,4 +401,5 @@ def decode_attention_fp8(q8, k8, v8, q_descale, k_descale, v_descale, scale=None
     return out, lse
 
 
+from .paged import copy_pages, paged_append, paged_decode_attention  # noqa: E402
 from .rotary import qk_rotary, qk_rotary_bwd, rotary_frequencies  # noqa: E402

@@ -1,0 +1,526 @@
+"""GPU parity of paged_append, paged_decode_attention and copy_pages against the
+fp64 oracles (oracle/rotary.py, oracle/paged.py).
+
+Tolerances of the attention. A score is an fp32 sum of d exact products: off by
+at most e = scale d 2^-23 sum |q_i k_i| (each addition by one unit, truncating),
+and each exponential by 2^-21 relative besides. lse is then off by at most
+e + 2^-20 plus the fp32 sums' chains (under 2^12 additions a thread, then trees):
+2^-12 at the very worst, in practice far less; the bound takes 2^-17 for chains
+under 2^7. The weights are off by the rounding of p, u = 2^-8 (bf16) or 2^-11
+(f16), e and 2^-21, in numerator and normaliser: O by twice that times
+sum w |v - O|. f16 probabilities under 2^-14 are off by 2^-25 each instead:
+sum |v - O| / sum exp. The fp32 sums of O add 2^-17 sum w |v|, the last rounding
+2^-8 |O|. Append: see tests/test_rotary_gpu.py; an e4m3 code is off by half a
+step, 2^-4 of the value or 2^-10 among subnormals."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import paged as opaged
+from oracle import rotary as orot
+from tests.test_rotary_gpu import DEV, TINY, U, fa, np64, partner_sum, weights  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+E4M3 = torch.float8_e4m3fn
+
+
+def pages_of(P, H_kv, page, d, elem, token_major=False, seed=0, ks=0.02, vs=0.01, mult=1.0):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    shape = (P, page, H_kv, d) if token_major else (P, H_kv, page, d)
+    out = []
+    for s in (ks, vs):
+        x = torch.randn(shape, generator=g, device=DEV) * mult
+        x = (x / s).clamp(-448, 448).to(E4M3) if elem == 1 else x.to(torch.bfloat16)
+        out.append(x.transpose(1, 2) if token_major else x)
+    return out[0], out[1], (ks if elem == 1 else 1.0), (vs if elem == 1 else 1.0)
+
+
+def decode_and_check(fa, q, kc, vc, ks, vs, table, lens, what="", scale=None, **kw):
+    d = q.shape[-1]
+    o, lse = fa.paged_decode_attention(q, kc, vc, table, lens, scale=scale, k_descale=ks,
+                                       v_descale=vs, **kw)
+    torch.cuda.synchronize()
+    scale = 1 / math.sqrt(d) if scale is None else scale
+    ro, rl, x = opaged.decode(np64(q)[:, :, 0], np64(kc) * ks, np64(vc) * vs,
+                              table.cpu().numpy(), lens.cpu().numpy(), scale)
+    e = scale * d * 2.0 ** -23 * x["mag"]
+    empty = np.isneginf(rl)
+    gl, go = np64(lse)[..., 0], np64(o)[:, :, 0]
+    assert np.array_equal(np.isneginf(gl), empty), what
+    lerr = np.abs(gl[~empty] - rl[~empty])
+    assert np.all(lerr <= (e + 2.0 ** -20 + 2.0 ** -17)[~empty] + U * np.abs(rl[~empty])), \
+        f"{what}: lse {lerr.max()}"
+    u = 2.0 ** -8 if kc.dtype == torch.bfloat16 else 2.0 ** -11
+    tol = 2 * (u + e[..., None] + 2.0 ** -21) * x["dev"] + 2.0 ** -17 * x["absv"] \
+        + 2.0 ** -8 * np.abs(ro) + TINY
+    if kc.dtype != torch.bfloat16:
+        tol = tol + 2.0 ** -24 * x["flat"]
+    err = np.abs(go - ro)
+    assert np.all(err <= tol), f"{what}: O off by {err.max()} ({(err - tol).max()} over)"
+    return o, lse
+
+
+def shuffled_table(P, B, width, seed=0):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randperm(P, generator=g)[:B * width].view(B, width).to(torch.int32).to(DEV)
+
+
+def queries(B, H, d, seed=1, mult=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(B, H, 1, d, generator=g) * mult).to(torch.bfloat16).to(DEV)
+
+
+HEADS = [(1, 1), (4, 4), (6, 2), (8, 1), (9, 1), (16, 1), (20, 1), (40, 2)]
+
+
+@pytest.mark.parametrize("elem", [2, 1])
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("H,H_kv", HEADS)
+def test_decode_heads(fa, H, H_kv, d, elem):  # noqa: F811
+    """Every head grouping on both sides of the 8- and 16-head tiles, lengths
+    0, 1 and around the tiles."""
+    lens = [0, 1, 15, 16, 17, 63, 64, 65, 127, 128, 129, 300]
+    B, page = len(lens), 16
+    width = -(-max(lens) // page)
+    kc, vc, ks, vs = pages_of(B * width + 3, H_kv, page, d, elem, seed=d + H)
+    decode_and_check(fa, queries(B, H, d), kc, vc, ks, vs, shuffled_table(B * width + 3, B, width),
+                     torch.tensor(lens, dtype=torch.int32, device=DEV), f"H{H} H_kv{H_kv} d{d}")
+
+
+@pytest.mark.parametrize("elem", [2, 1])
+@pytest.mark.parametrize("token_major", [False, True])
+@pytest.mark.parametrize("page", [1, 3, 8, 24, 128, 200])
+def test_decode_pages(fa, page, token_major, elem):  # noqa: F811
+    """Page sizes that end inside a tile and hold several; both page orders."""
+    lens = [37, 513, 1, 200]
+    width = -(-max(lens) // page)
+    P = 4 * width + 2
+    kc, vc, ks, vs = pages_of(P, 2, page, 128, elem, token_major, seed=page)
+    decode_and_check(fa, queries(4, 8, 128), kc, vc, ks, vs, shuffled_table(P, 4, width, page),
+                     torch.tensor(lens, dtype=torch.int32, device=DEV), f"page {page}")
+
+
+@pytest.mark.parametrize("elem", [2, 1])
+def test_decode_shared_out(fa, elem):  # noqa: F811
+    """One long sequence over all blocks among short ones, and a tail."""
+    lens = [3, 9000, 40, 0, 7, 1111]
+    width = -(-9000 // 32)
+    kc, vc, ks, vs = pages_of(6 * width, 2, 32, 128, elem, seed=4)
+    decode_and_check(fa, queries(6, 8, 128), kc, vc, ks, vs, shuffled_table(6 * width, 6, width),
+                     torch.tensor(lens, dtype=torch.int32, device=DEV))
+
+
+def test_decode_many_sequences(fa):  # noqa: F811
+    """More sequences than threads of a block (several a thread in the scan)."""
+    rng = np.random.default_rng(0)
+    B, width = 700, 3
+    lens = rng.integers(0, 40, B).astype(np.int32)
+    kc, vc, _, _ = pages_of(B * width, 1, 16, 64, 2, seed=5)
+    decode_and_check(fa, queries(B, 2, 64), kc, vc, 1.0, 1.0, shuffled_table(B * width, B, width),
+                     torch.from_numpy(lens).to(DEV))
+
+
+@pytest.mark.parametrize("elem", [2, 1])
+def test_decode_hidden_slots_hold_anything(fa, elem):  # noqa: F811
+    """NaN in every slot past a sequence's length and in every page that no
+    sequence lists; table entries past the length that name no page."""
+    B, page, width = 3, 16, 8
+    lens = torch.tensor([5, 33, 100], dtype=torch.int32, device=DEV)
+    kc, vc, ks, vs = pages_of(B * width + 4, 2, page, 128, elem, seed=6)
+    table = shuffled_table(B * width + 4, B, width)
+    used = torch.zeros(B * width + 4, page, dtype=torch.bool, device=DEV)
+    for b in range(B):
+        for j in range(int(lens[b])):
+            used[table[b, j // page], j % page] = True
+    for c in (kc, vc):
+        raw = c.view(torch.uint8) if elem == 1 else c.view(torch.int16)
+        nan = 0x7F if elem == 1 else 0x7FC0
+        raw.masked_fill_(~used[:, None, :, None], nan)
+    for b in range(B):
+        last = -(-int(lens[b]) // page)
+        table[b, last:] = torch.tensor([-1, 1 << 30], dtype=torch.int32).repeat(8)[:width - last]
+    o, _ = decode_and_check(fa, queries(B, 6, 128), kc, vc, ks, vs, table, lens)
+    assert torch.isfinite(o).all()
+
+
+def test_decode_bad_pages_hide_keys(fa):  # noqa: F811
+    """A listed page outside the cache hides its keys; a sequence with no other
+    is empty; kv_len is clamped to the table's width and to 0."""
+    kc, vc, _, _ = pages_of(12, 2, 16, 64, 2, seed=7)
+    table = torch.tensor([[0, -1, 2], [99, -5, 12], [3, 4, 5], [6, 7, 8]], dtype=torch.int32,
+                         device=DEV)
+    lens = torch.tensor([45, 48, 1000000, -3], dtype=torch.int32, device=DEV)
+    o, lse = fa.paged_decode_attention(queries(4, 4, 64), kc, vc, table, lens)
+    clamped = torch.tensor([45, 48, 48, 0], dtype=torch.int32, device=DEV)
+    o2, lse2 = decode_and_check(fa, queries(4, 4, 64), kc, vc, 1.0, 1.0, table, clamped)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    for b in (1, 3):
+        assert (o[b] == 0).all() and torch.isneginf(lse[b]).all()
+
+
+@pytest.mark.parametrize("elem", [2, 1])
+def test_decode_moving_reference(fa, elem):  # noqa: F811
+    """Scores that rise by 16 log2 units from one 16-key group to the next, and
+    fall again: the reference moves in every group; and flat scores."""
+    d, n, page = 128, 640, 16
+    kc, vc, ks, vs = pages_of(n // page, 1, page, d, elem, seed=8, ks=1.0, vs=0.01)
+    step = torch.cat([torch.arange(20), torch.arange(20).flip(0)]).float()
+    k = torch.zeros(n // page, 1, page, d, device=DEV)
+    k[..., 0] = (step[:n // page, None, None] * 2).to(DEV)
+    kc = k.to(E4M3 if elem == 1 else torch.bfloat16)
+    q = torch.zeros(1, 4, 1, d, device=DEV)
+    q[..., 0] = torch.tensor([1.0, 64.0, 512.0, -64.0], device=DEV)[None, :, None]
+    table = torch.arange(n // page, dtype=torch.int32, device=DEV)[None]
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    decode_and_check(fa, q.to(torch.bfloat16), kc, vc, 1.0, vs, table, lens)
+
+
+@pytest.mark.parametrize("mult", [2.0 ** -60, 2.0 ** 60, 0.0])
+def test_decode_e4m3_query_range(fa, mult):  # noqa: F811
+    """Queries far outside f16's range: the power-of-two scaling keeps them."""
+    kc, vc, ks, vs = pages_of(8, 1, 16, 128, 1, seed=9)
+    q = queries(1, 5, 128, mult=mult)
+    scale = 0.1 / mult if mult else 0.1
+    table = torch.arange(8, dtype=torch.int32, device=DEV)[None]
+    lens = torch.tensor([120], dtype=torch.int32, device=DEV)
+    decode_and_check(fa, q, kc, vc, ks, vs, table, lens, scale=scale)
+
+
+def test_decode_nan_queries_and_visible_nan(fa):  # noqa: F811
+    """A NaN in one head's query or in a visible key or value reaches the rows
+    that use it and no others."""
+    kc, vc, _, _ = pages_of(60, 2, 16, 64, 2, seed=10)
+    q = queries(3, 4, 64)
+    q[0, 1] = float("nan")
+    kc[5, 1, 3, 7] = float("nan")        # in sequences 0 and 1, heads 2 and 3
+    vc[45, 0, 2, 9] = float("nan")       # sequence 2, heads 0 and 1, column 9
+    table = torch.arange(60, dtype=torch.int32, device=DEV).view(3, 20)
+    table[1, 0] = 5
+    lens = torch.tensor([300, 300, 300], dtype=torch.int32, device=DEV)
+    o, lse = fa.paged_decode_attention(q, kc, vc, table, lens)
+    bad = torch.isnan(lse[..., 0]).nonzero().tolist()
+    assert bad == [[0, 1], [0, 2], [0, 3], [1, 2], [1, 3]]
+    assert torch.isnan(o[0, 1]).all() and torch.isnan(o[1, 2:]).all()
+    assert torch.isnan(o[2, :2, 0, 9]).all()
+    o[2, :2, 0, 9] = 0
+    assert torch.isfinite(o[2]).all() and torch.isfinite(o[1, :2]).all()
+
+
+def test_decode_views_and_outputs(fa):  # noqa: F811
+    """q as heads of a fused buffer, K and V as slices of one tensor, table rows
+    cut from a wider one, caller's outputs and workspace, repeated calls equal."""
+    B, H, H_kv, d, page = 5, 8, 2, 128, 16
+    both = torch.randn(30, 2, H_kv, page, d, device=DEV).to(torch.bfloat16)
+    kc, vc = both[:, 0], both[:, 1]
+    fused = torch.randn(B, 1, H + 2 * H_kv, d, device=DEV).to(torch.bfloat16).transpose(1, 2)
+    q = fused[:, :H]
+    table = shuffled_table(30, 6, 5)[:, 1:4]
+    lens = torch.tensor([48, 1, 20, 33, 0], dtype=torch.int32, device=DEV)
+    ws = torch.full((fa.load_library().fa_paged_decode_workspace_bytes(B, H, H_kv, d),), 0xFF,
+                    dtype=torch.uint8, device=DEV)
+    out = torch.empty(B, H, 1, d, dtype=torch.bfloat16, device=DEV)
+    lse = torch.empty(B, H, 1, device=DEV)
+    a = decode_and_check(fa, q, kc, vc, 1.0, 1.0, table, lens, workspace=ws, out=out, lse=lse)
+    assert a[0] is out and a[1] is lse
+    o2, l2 = fa.paged_decode_attention(q, kc, vc, table, lens, workspace=ws)
+    assert torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+def test_decode_offsets_beyond_32_bits(fa):  # noqa: F811
+    """Pages more than 2^32 bytes and 2^31 elements into the cache."""
+    P, H_kv, page, d = 150000, 8, 16, 128
+    kc = torch.empty(P, H_kv, page, d, dtype=torch.bfloat16, device=DEV)
+    vc = torch.empty_like(kc)
+    assert kc.numel() > 1 << 31
+    small_k, small_v, _, _ = pages_of(8, H_kv, page, d, 2, seed=11)
+    where = torch.tensor([149999, 140000, 131072, 131071, 3, 149998, 70000, 0], device=DEV)
+    q = queries(1, 16, d)
+    lens = torch.tensor([121], dtype=torch.int32, device=DEV)
+    # the pages get there by copies from the cache's start, as compaction makes them
+    kc[100:108], vc[100:108] = small_k, small_v
+    fa.copy_pages(kc, vc, torch.arange(100, 108, dtype=torch.int32, device=DEV),
+                  where.to(torch.int32))
+    assert torch.equal(kc[where], small_k) and torch.equal(vc[where], small_v)
+    o, lse = fa.paged_decode_attention(q, kc, vc, where.to(torch.int32)[None], lens)
+    o2, lse2 = decode_and_check(fa, q, small_k, small_v, 1.0, 1.0,
+                                torch.arange(8, dtype=torch.int32, device=DEV)[None], lens)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    new = torch.randn(1, H_kv, 1, d, device=DEV).to(torch.bfloat16)
+    pos = torch.tensor([[121]], dtype=torch.int32, device=DEV)
+    fa.paged_append(new, new, kc, vc, where.roll(1).to(torch.int32)[None], pos)
+    assert torch.equal(kc[70000, :, 9], new[0, :, 0])
+
+
+# ---------------------------------------------------------------- append
+def check_stored(got, ref, descale, elem, mag):
+    """Stored values (codes, before descale) against fp64 values."""
+    want = ref / descale
+    extra = 32 * U * mag / descale
+    if elem == 2:
+        tol = 2.0 ** -8 * np.abs(want) + extra + TINY
+    else:
+        want = np.clip(want, -448, 448)
+        tol = np.maximum(2.0 ** -4 * np.abs(want), 2.0 ** -10) + extra + 2.0 ** -22 * np.abs(want)
+    assert np.all(np.abs(got - want) <= tol), np.abs(got - want).max()
+
+
+APPENDS = [  # B, H, H_kv, N, d, page, rot, norm, inter, elem, token_major
+    (1, 1, 1, 1, 64, 16, 64, False, False, 2, False),
+    (16, 32, 8, 1, 128, 16, 128, True, False, 2, False),
+    (3, 6, 2, 37, 128, 24, 32, True, True, 1, True),
+    (2, 4, 4, 100, 256, 8, 256, False, False, 1, False),
+    (2, 0, 3, 19, 64, 1, 16, True, False, 2, True),
+    (5, 8, 1, 3, 64, 64, 0, False, False, 1, False),
+    (130, 2, 1, 1, 256, 16, 64, True, True, 2, False),
+]
+
+
+@pytest.mark.parametrize("B,H,H_kv,N,d,page,rot,norm,inter,elem,token_major", APPENDS)
+def test_append(fa, B, H, H_kv, N, d, page, rot, norm, inter, elem, token_major):  # noqa: F811
+    """New tokens at ragged starts; slots that no token goes to, and q_out rows
+    of padding, stay as they were bit for bit."""
+    g = torch.Generator().manual_seed(B + N)
+    x = torch.randn(B, N, H + 2 * H_kv, d, generator=g).to(torch.bfloat16).to(DEV).transpose(1, 2)
+    q, k, v = x[:, :H], x[:, H:H + H_kv], x[:, H + H_kv:]
+    rng = np.random.default_rng(B)
+    start = rng.integers(0, 200, B)
+    pos = (start[:, None] + np.arange(N)).astype(np.int32)
+    if N > 2:
+        pos[:, -1] = -1                                      # padding
+        pos[0, 0] = -7
+    width = -(-(200 + N) // page)
+    P = B * width + 2
+    table = shuffled_table(P, B, width, seed=N)
+    kc, vc, ks, vs = pages_of(P, H_kv, page, d, elem, token_major, seed=1)
+    k0, v0 = kc.clone(), vc.clone()
+    eps = 1e-6 if norm else None
+    wq, wk = weights(d, False) if norm else (None, None)
+    freqs = fa.rotary_frequencies(rot) if rot else None
+    f64 = np64(freqs) if rot else np.zeros(0)
+    q_out = torch.full((B, H, N, d), 7.0, dtype=torch.bfloat16, device=DEV)
+    got = fa.paged_append(k, v, kc, vc, table, torch.from_numpy(pos).to(DEV),
+                          q=q if H else None, freqs=freqs, interleaved=inter, norm_eps=eps,
+                          q_weight=wq, k_weight=wk, k_descale=ks, v_descale=vs,
+                          q_out=q_out if H else None)
+    torch.cuda.synchronize()
+    live = pos >= 0
+    if H:
+        assert got is q_out
+        w64 = None if wq is None else np64(wq)
+        ref = orot.forward(np64(q), pos, f64, inter, 1.0, eps, w64)
+        mag = partner_sum(orot.norm(np64(q), eps, w64), len(f64), inter)
+        o = np64(q_out)
+        tol = 2.0 ** -8 * np.abs(ref) + 32 * U * mag + TINY
+        rows = np.broadcast_to(live[:, None], (B, H, N))
+        assert np.all((np.abs(o - ref) <= tol)[rows])
+        assert np.all(o[~rows] == 7.0)
+    else:
+        assert got is None
+    wk64 = None if wk is None else np64(wk)
+    rk = orot.forward(np64(k), pos, f64, inter, 1.0, eps, wk64)
+    mk = partner_sum(orot.norm(np64(k), eps, wk64), len(f64), inter)
+    b, n = np.nonzero(live)
+    page_of = table.cpu().numpy()[b, pos[b, n] // page]
+    slot = pos[b, n] % page
+    at = (torch.from_numpy(page_of).long().to(DEV), slice(None), torch.from_numpy(slot).to(DEV))
+
+    def raw(c):
+        return c.view(torch.uint8) if elem == 1 else c
+
+    check_stored(raw(kc)[at].view(kc.dtype).double().cpu().numpy(), rk[b, :, n], ks, elem,
+                 mk[b, :, n])
+    if elem == 2:
+        assert torch.equal(vc[at], v[torch.from_numpy(b).to(DEV), :, torch.from_numpy(n).to(DEV)])
+    else:
+        check_stored(raw(vc)[at].view(vc.dtype).double().cpu().numpy(), np64(v)[b, :, n], vs, elem,
+                     0 * mk[b, :, n])
+    for c, c0 in ((kc, k0), (vc, v0)):                       # everything else untouched
+        raw(c0)[at] = raw(c)[at]
+        assert torch.equal(raw(c), raw(c0))
+
+
+def test_append_special_values(fa):  # noqa: F811
+    """e4m3 saturates (infinities too) and keeps NaN; bf16 keeps them all."""
+    d = 64
+    k = torch.zeros(1, 1, 1, d, dtype=torch.bfloat16, device=DEV)
+    vals = [float("inf"), float("-inf"), float("nan"), 1000.0, -449.0, 448.0, 2.0 ** -9, 1e-4]
+    k[0, 0, 0, :8] = torch.tensor(vals)
+    pos = torch.zeros(1, 1, dtype=torch.int32, device=DEV)
+    table = torch.zeros(1, 1, dtype=torch.int32, device=DEV)
+    kc = torch.zeros(1, 1, 4, d, dtype=E4M3, device=DEV)
+    vc = torch.zeros_like(kc)
+    fa.paged_append(k, k, kc, vc, table, pos)
+    for c in (kc, vc):
+        got = c[0, 0, 0, :8].float().tolist()
+        assert got[:2] == [448.0, -448.0] and math.isnan(got[2])
+        assert got[3:7] == [448.0, -448.0, 448.0, 2.0 ** -9] and got[7] == 0.0
+    kb = torch.zeros(1, 1, 4, d, dtype=torch.bfloat16, device=DEV)
+    vb = torch.zeros_like(kb)
+    fa.paged_append(k, k, kb, vb, table, pos)
+    for c in (kb, vb):
+        assert torch.equal(c[0, 0, 0].view(torch.int16), k[0, 0, 0].view(torch.int16))
+
+
+def test_append_drops_what_has_no_page(fa):  # noqa: F811
+    """Unknown sequences, positions past the table and bad pages write nothing
+    to the cache; their queries come out all the same."""
+    kc, vc, _, _ = pages_of(6, 2, 8, 64, 2, seed=2)
+    k0, v0 = kc.clone(), vc.clone()
+    x = torch.randn(6, 4, 1, 64, device=DEV).to(torch.bfloat16)
+    table = torch.tensor([[0, 1], [-1, 6], [2, 1 << 29]], dtype=torch.int32, device=DEV)
+    seq = torch.tensor([3, -1, 0, 1, 1, 2], dtype=torch.int32, device=DEV)
+    pos = torch.tensor([[0], [0], [16], [3], [9], [8]], dtype=torch.int32, device=DEV)
+    q = fa.paged_append(x[:, :2], x[:, 2:], kc, vc, table, pos, q=x, seq=seq)
+    assert torch.equal(q, x) and torch.equal(kc, k0) and torch.equal(vc, v0)
+    seq[0], pos[0] = 2, 5
+    fa.paged_append(x[:, :2], x[:, 2:], kc, vc, table, pos, seq=seq)
+    assert torch.equal(kc[2, :, 5], x[0, :2, 0]) and torch.equal(vc[2, :, 5], x[0, 2:, 0])
+    far = torch.full((6, 1), (1 << 31) - 1, dtype=torch.int32, device=DEV)
+    fa.paged_append(x[:, :2], x[:, 2:], kc, vc, table, far)
+
+
+# ---------------------------------------------------------------- copies
+@pytest.mark.parametrize("elem", [2, 1])
+@pytest.mark.parametrize("H_kv,page,d", [(1, 1, 64), (3, 5, 64), (2, 16, 128), (8, 64, 256)])
+@pytest.mark.parametrize("layout", ["heads", "tokens", "padded"])
+def test_copy(fa, H_kv, page, d, elem, layout):  # noqa: F811
+    P = 41
+    kc, vc, _, _ = pages_of(P, H_kv, page, d, elem, layout == "tokens", seed=3)
+    if layout == "padded":                                   # rows wider than a head
+        wide = [torch.zeros(P, H_kv, page + 1, d + 16, device=DEV).to(kc.dtype) for _ in range(2)]
+        for w, c in zip(wide, (kc, vc)):
+            w[:, :, :page, :d] = c
+        kc, vc = (w[:, :, :page, :d] for w in wide)
+    g = torch.Generator().manual_seed(page)
+    perm = torch.randperm(P, generator=g).to(torch.int32).to(DEV)
+    src, dst = perm[:15].clone(), perm[20:35].clone()
+    src[3] = src[2]                                          # one source, two copies
+    src[7] = dst[7]                                          # onto itself
+    src[9], dst[11] = -1, P                                  # skipped
+
+    def raw(c):
+        return c.view(torch.uint8) if elem == 1 else c
+
+    want = [raw(c).clone() for c in (kc, vc)]
+    for w, c in zip(want, (kc, vc)):
+        for i, (s, t) in enumerate(zip(src.tolist(), dst.tolist())):
+            if 0 <= s < P and 0 <= t < P:
+                w[t] = raw(c)[s]
+    fa.copy_pages(kc, vc, src, dst)
+    for w, c in zip(want, (kc, vc)):
+        assert torch.equal(raw(c), w)
+    if layout == "padded":
+        assert all((w[:, :, page:].float() == 0).all() and (w[..., d:].float() == 0).all()
+                   for w in wide)
+
+
+# ---------------------------------------------------------------- together
+@pytest.mark.parametrize("elem", [2, 1])
+def test_prompt_fork_decode_compact(fa, elem):  # noqa: F811
+    """A serving run: two prompts appended as one padded batch; the second forked
+    (full pages shared, the last one copied); three sequences decode two tokens
+    each; the live pages are moved down and decoding gives the same bits. Each
+    step's attention is checked on the cache as it stands, and, for bf16, the
+    cache against the contiguous path."""
+    H, H_kv, d, page, P = 8, 2, 128, 16, 64
+    kc, vc, ks, vs = pages_of(P, H_kv, page, d, elem, seed=5)
+    freqs = fa.rotary_frequencies(128, scaling="linear", factor=2.0)
+    wq, wk = weights(d, False)
+    kw = dict(freqs=freqs, norm_eps=1e-6, q_weight=wq, k_weight=wk, k_descale=ks, v_descale=vs)
+    g = torch.Generator().manual_seed(9)
+    lens = [45, 70]
+    x = torch.randn(2, 70, H + 2 * H_kv, d, generator=g).to(torch.bfloat16).to(DEV).transpose(1, 2)
+    pos = torch.arange(70, dtype=torch.int32).repeat(2, 1)
+    pos[0, 45:] = -1
+    table = torch.full((3, 8), -1, dtype=torch.int32)
+    order = iter(np.random.default_rng(1).permutation(P).tolist())
+    for b, n in enumerate(lens):
+        for i in range(-(-n // page)):
+            table[b, i] = next(order)
+    table = table.to(DEV)
+    fa.paged_append(x[:, H:H + H_kv], x[:, H + H_kv:], kc, vc, table, pos.to(DEV), q=x[:, :H], **kw)
+    # fork sequence 1: four full pages shared, page 4 copied
+    table[2] = table[1]
+    table[2, 4] = next(order)
+    fa.copy_pages(kc, vc, table[1, 4:5].clone(), table[2, 4:5].clone())
+    kv_len = torch.tensor([45, 70, 70], dtype=torch.int32, device=DEV)
+    fresh = []
+    for step in range(2):
+        y = torch.randn(3, 1, H + 2 * H_kv, d, generator=g).to(torch.bfloat16).to(DEV).transpose(1, 2)
+        for b in range(3):
+            if int(kv_len[b]) % page == 0:
+                table[b, int(kv_len[b]) // page] = next(order)
+        q = fa.paged_append(y[:, H:H + H_kv], y[:, H + H_kv:], kc, vc, table, kv_len[:, None],
+                            q=y[:, :H], **kw)
+        kv_len += 1
+        o, lse = decode_and_check(fa, q, kc, vc, ks, vs, table, kv_len, f"step {step}")
+        fresh.append(y)
+    assert not torch.equal(o[1], o[2])                       # the fork went its own way
+    # compaction: every live page to a free page below the live count
+    live = torch.unique(table[table >= 0])
+    n = len(live)
+    low = torch.zeros(P, dtype=torch.bool, device=DEV)
+    low[live.long()] = True
+    src = live[live >= n]
+    dst = (~low[:n]).nonzero().flatten().to(torch.int32)
+    assert len(src) == len(dst) > 0
+    fa.copy_pages(kc, vc, src, dst)
+    new_id = torch.arange(P, dtype=torch.int32, device=DEV)
+    new_id[src.long()] = dst
+    moved = torch.where(table >= 0, new_id[table.clamp(min=0).long()], table)
+    assert int(moved.max()) < n
+    o2, lse2 = fa.paged_decode_attention(q, kc, vc, moved, kv_len, k_descale=ks, v_descale=vs)
+    assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    if elem == 2:
+        # the contiguous path over the same keys (sequence 0): qk_rotary + decode_attention
+        ks_all = torch.cat([x[:1, H:H + H_kv, :45]] + [y[:1, H:H + H_kv] for y in fresh], 2)
+        vs_all = torch.cat([x[:1, H + H_kv:, :45]] + [y[:1, H + H_kv:] for y in fresh], 2)
+        _, kr = fa.qk_rotary(ks_all[:, :0], ks_all, torch.arange(47, dtype=torch.int32, device=DEV),
+                             freqs, norm_eps=1e-6, q_weight=wq, k_weight=wk)
+        oc, lc = fa.decode_attention(q[:1].contiguous(), kr.contiguous(), vs_all.contiguous())
+        assert (oc.float() - o[:1].float()).abs().max() <= 2e-2
+        assert (lc - lse[:1]).abs().max() <= 1e-3
+
+
+def test_streams_and_graphs(fa):  # noqa: F811
+    """Decoding on a named stream; two captured steps (append, then attention)
+    replayed in turn, each with its own workspace, over a growing cache."""
+    B, H, H_kv, d, page = 4, 8, 2, 128, 16
+    kc, vc, _, _ = pages_of(200, H_kv, page, d, 2, seed=6)
+    table = shuffled_table(200, B, 40)
+    kv_len = torch.tensor([5, 300, 600, 1], dtype=torch.int32, device=DEV)
+    q = queries(B, H, d)
+    want = fa.paged_decode_attention(q, kc, vc, table, kv_len)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = fa.paged_decode_attention(q, kc, vc, table, kv_len, stream=side.cuda_stream)
+    side.synchronize()
+    assert torch.equal(want[0], got[0]) and torch.equal(want[1], got[1])
+
+    new = torch.randn(B, H + 2 * H_kv, 1, d, device=DEV).to(torch.bfloat16)
+    freqs = fa.rotary_frequencies(64)
+
+    def step():
+        qq = fa.paged_append(new[:, H:H + H_kv], new[:, H + H_kv:], kc, vc, table, kv_len[:, None],
+                             q=new[:, :H], freqs=freqs)
+        n = kv_len + 1
+        return (*fa.paged_decode_attention(qq, kc, vc, table, n), n)
+
+    step()
+    torch.cuda.synchronize()
+    graphs, kept = [], []
+    for _ in range(2):
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            kept.append(step())
+        graphs.append(gr)
+    for i in range(4):
+        new.copy_(torch.randn(B, H + 2 * H_kv, 1, d, device=DEV).to(torch.bfloat16))
+        graphs[i % 2].replay()
+        o, lse, n = kept[i % 2]
+        decode_and = step()
+        assert torch.equal(o, decode_and[0]) and torch.equal(lse, decode_and[1])
+        kv_len.copy_(n)
