@@ -159,7 +159,7 @@ PdPlan pd_plan(int B, int H, int H_kv, int d) {
     pl.G = H / H_kv;
     pl.nt = head_tiles(pl.G);
     pl.hblk = (pl.G + 8 * pl.nt - 1) / (8 * pl.nt);
-    const size_t rows = (size_t)kPdBlocks * 2 * 8 * pl.nt;
+    const size_t rows = (size_t)kPdBlocks * 2 * kPdWarpsMost * 8 * pl.nt;
     pl.o_bytes = rows * d * 4;
     pl.lse_bytes = up256(rows * 4);
     pl.split_bytes = up256((size_t)B * H_kv * pl.hblk * 8);
@@ -182,19 +182,17 @@ int launch_decode(const PdParams& p, cudaStream_t s) {
     }
     kern<<<kPdBlocks, C::kThreads, C::kSmem, s>>>(p);
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_LAUNCH;
-    // No sequence can be longer than the table is wide: where that is one
-    // tile, no unit is shared and there is nothing to join.
-    if ((int64_t)p.width * p.page_size <= C::kKeys) return FA_OK;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(((int64_t)p.B * p.H + kPdJoinWarps - 1) / kPdJoinWarps));
-    cfg.blockDim = dim3(32 * kPdJoinWarps);
+    cfg.gridDim = dim3((unsigned)((int64_t)p.B * p.H));
+    cfg.blockDim = dim3(kPdJoinThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, fa_paged_join<D>, p, (int)C::kHeads);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fa_paged_join<D>, p, (int)C::kHeads,
+                                             (int)C::kWarps);
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
@@ -254,6 +252,15 @@ int decode(const fa_paged_decode_t& a, void* ws, size_t ws_bytes, void* stream) 
     p.width = a.table.pages_per_seq;
     p.num_pages = c.num_pages;
     p.page_size = c.page_size;
+    // key / page_size = (2 key * m) >> 32 >> s for keys below 2^31, with s =
+    // ceil(log2 page_size) and m = ceil(2^(31 + s) / page_size) < 2^32: the
+    // excess of m is below page_size / 2^(31 + s), so key times it stays below
+    // one unit of 1 / page_size.
+    uint32_t lg = 0;
+    while ((1ll << lg) < c.page_size) ++lg;
+    p.page_mul = (uint32_t)(((1ull << (31 + lg)) + c.page_size - 1) / c.page_size);
+    p.page_shift = lg;
+    p.whole16 = c.page_size % 16 == 0;
     p.kv_len = a.kv_len;
     p.o = static_cast<__nv_bfloat16*>(a.o);
     p.lse = a.lse;

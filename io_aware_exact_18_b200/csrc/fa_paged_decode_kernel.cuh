@@ -9,22 +9,27 @@
 // SM has loads in flight all the time, whatever the sequences' lengths.
 //
 // Work split. A unit is (sequence, K/V head, block of up to 8 NT query heads),
-// cut into tiles of kKeys keys; the tiles of ALL units, laid end to end, are
-// shared out evenly over the blocks (one an SM), so ragged lengths balance to
-// one tile and a single long sequence fills the chip. A block's range covers
-// the end of one unit, whole units, and the start of another: only the first
-// and the last can be shared with other blocks, so a block leaves at most two
-// partial results (normalised O and log-sum-exp in fp32), whatever the
-// lengths, and fa_paged_join merges a unit's parts in block order.
+// cut into steps of kStep keys; the steps of ALL units, laid end to end, are
+// shared out evenly over all WARPS of the grid (kWarps a block, one block an
+// SM), so ragged lengths balance to one step, one long sequence fills the chip
+// and many short ones cost no block-wide hand-over. A warp's range covers the
+// end of one unit, whole units, and the start of another. Whole units are
+// finished in registers. A unit that ends in a later warp than it began in
+// leaves partial results (normalised O and log-sum-exp, fp32): one from the
+// warp that ends it, and one a block from the warps that are still inside it
+// when their ranges end, joined in shared memory once, at the block's end.
+// fa_paged_join adds a unit's parts in order. A block leaves at most 2 kWarps
+// parts whatever the lengths, so the workspace does not grow with them.
 //
-// Inside a block every warp works alone on 16 keys of each tile, with a ring
-// of kStages (K, V) stages of its own that its lanes fill with 16-byte
-// cp.async: no block barrier in the loop. Each lane looks up the page of one
-// key (table entries are fetched one tile ahead) and the row's offset goes
-// round by shuffle, so any page size and page order costs the same; a key
-// that is hidden or has no page is zero-filled and its score set to -inf,
-// never read, so what lies there cannot reach the result. Rings continue
-// across unit boundaries.
+// A warp has a ring of kStages (K, V) steps of its own that its lanes fill
+// with 16-byte cp.async, and it runs on across unit boundaries: there is no
+// block barrier before the end. Lanes look up the pages of the next step while
+// the present one is computed: where page_size is a multiple of 16, one page
+// for 16 keys, whose rows then follow at a fixed stride; otherwise one key a
+// lane, the row offsets going round by shuffle (measured on the e4m3 batch of
+// 32 ragged sequences of up to 8192 keys: @PAGES@). A key that is hidden or
+// has no page is zero-filled and its score set to -inf, never read, so what
+// lies there cannot reach the result.
 //
 // Products (mma.sync m16n8k16, fp32 accumulators): S^T = K Q^T with the keys
 // as rows and 8 query heads as columns, then O^T += V^T P^T. The C fragment of
@@ -51,24 +56,26 @@
 namespace fa {
 
 constexpr int kPdBlocks = 148;             // one block an SM
-constexpr int kPdPitch = 132;              // floats of a head's row in the merge buffer
 
 template <int D, int E, int NT>
 struct PdCfg {
     static constexpr int kRow = D * E;                                    // bytes of a K or V row
-    static constexpr int kStage = 2 * 16 * kRow;                          // K and V of 16 keys
+    static constexpr int kStep = kRow <= 128 ? 32 : 16;                   // keys of a step
+    static constexpr int kGroups = kStep / 16;
+    static constexpr int kStage = 2 * kStep * kRow;                       // K and V of a step
     static constexpr int kWarps = kRow >= 512 ? 4 : 8;
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kKeys = 16 * kWarps;                             // keys of a tile
-    static constexpr int kStages = kRow >= 256 ? 3 : kRow == 128 ? 6 : 8;
+    static constexpr int kStages = kRow >= 128 ? 3 : 6;
     static constexpr int kHeads = 8 * NT;
-    static constexpr int kCols = D < 128 ? D : 128;                       // of one merge pass
+    static constexpr int kPitch = D + 4;                                  // of the merge buffer
     static constexpr int kRing = kWarps * kStages * kStage;
-    static constexpr int kMerge = kWarps * 8 * kPdPitch * 4;
+    static constexpr int kMerge = kWarps * kHeads * kPitch * 4;           // in the ring's place
     static constexpr int kStat = 3 * kWarps * kHeads * 4;                 // m, l, lr
-    static constexpr int kSmem = kRing + kMerge + kStat + kWarps * kStages * 4;
-    static_assert(kSmem <= 227 * 1024, "shared memory per block");
+    static constexpr int kSmem = kRing + kStat + kWarps * kStages * 4;
+    static_assert(kMerge <= kRing, "the merge buffer reuses the ring");
+    static_assert(kSmem <= 226 * 1024, "shared memory per block");
 };
+constexpr int kPdWarpsMost = 8;
 
 struct PdParams {
     const __nv_bfloat16* q;
@@ -78,12 +85,17 @@ struct PdParams {
     const int32_t* table;
     int64_t table_stride;
     int width, num_pages, page_size;
+    uint32_t page_mul, page_shift;         // key / page_size = (2 key * page_mul) >> 32 >> page_shift
+    int whole16;                           // page_size % 16 == 0: 16 keys share a page
     const int32_t* kv_len;
     __nv_bfloat16* o;
     float* lse;
-    float* part_o;                         // [blocks][2][kHeads][D]
-    float* part_lse;                       // [blocks][2][kHeads], log2 units
-    int2* split;                           // [B][units]: first and last block, or (-1, -1)
+    // Parts: slot (block * 2 + 0) * kWarps + w is that of the unit warp w ended,
+    // slot (block * 2 + 1) * kWarps + w that of the warps from w on which are
+    // inside one unit at their ends.
+    float* part_o;                         // [blocks][2][kWarps][kHeads][D]
+    float* part_lse;                       // [blocks][2][kWarps][kHeads], log2 units
+    int2* split;                           // [B][units]: first and last warp, or (-1, -1)
     int B, H, H_kv, G, hblk;               // hblk: head blocks of a K/V head
     float scale_log2, o_mul;
 };
@@ -153,11 +165,20 @@ __device__ __forceinline__ uint32_t stage_at(int r, int c) {
     else return (uint32_t)(r * kRow + ((c ^ ((r >> 1) & 3)) << 4));
 }
 
-// Tiles of the sequence of length len (an empty one has one, so that its row
-// is written).
-template <int kKeys>
-__device__ __forceinline__ int tiles_of(int len) {
-    return len <= 0 ? 1 : (len + kKeys - 1) / kKeys;
+// Steps of a sequence of length len: its keys' and one more without keys. That
+// one stands for what a unit costs besides its keys (its query, its statistics
+// and its row), about a step's time, so that ranges of many short units are
+// not longer in time than others; and an empty sequence has a step to write
+// its row from.
+template <int kStep>
+__device__ __forceinline__ int steps_of(int len) {
+    return (len + kStep - 1) / kStep + 1;
+}
+
+// a / b for a >= 0, b > 0, by the 32-bit divider where both fit it.
+__device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
+    if (((uint64_t)(a | b) >> 32) == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+    return a / b;
 }
 
 __device__ __forceinline__ int seq_len(const PdParams& p, int b) {
@@ -165,20 +186,20 @@ __device__ __forceinline__ int seq_len(const PdParams& p, int b) {
     return (int)max((int64_t)0, min((int64_t)p.kv_len[b], most));
 }
 
-// A place in the line of tiles.
+// A place in the line of steps.
 struct PdCursor {
-    int b, unit, tile, n, len;
+    int b, unit, step, n, len;
 };
 
-template <int kKeys>
+template <int kStep>
 __device__ __forceinline__ void pd_next(const PdParams& p, PdCursor& c, int units) {
-    if (++c.tile < c.n) return;
-    c.tile = 0;
+    if (++c.step < c.n) return;
+    c.step = 0;
     if (++c.unit < units) return;
     c.unit = 0;
     if (++c.b < p.B) {
         c.len = seq_len(p, c.b);
-        c.n = tiles_of<kKeys>(c.len);
+        c.n = steps_of<kStep>(c.len);
     }
 }
 
@@ -187,108 +208,143 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
     fa_paged_decode_kernel(const PdParams p) {
     using C = PdCfg<D, E, NT>;
     extern __shared__ __align__(128) uint8_t smem[];
-    float* merge = reinterpret_cast<float*>(smem + C::kRing);             // [warp][8][kPdPitch]
-    float* st_m = reinterpret_cast<float*>(smem + C::kRing + C::kMerge);  // [warp][kHeads]
+    float* st_m = reinterpret_cast<float*>(smem + C::kRing);              // [warp][kHeads]
     float* st_l = st_m + C::kWarps * C::kHeads;
     float* st_lr = st_l + C::kWarps * C::kHeads;
     uint32_t* seen = reinterpret_cast<uint32_t*>(st_lr + C::kWarps * C::kHeads);
-    __shared__ int64_t s_scan[C::kWarps];
-    __shared__ int64_t s_at;
-    __shared__ int s_b;
+    __shared__ int64_t s_open[C::kWarps];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int units = p.H_kv * p.hblk;
     pdl_launch_dependents();
 
     // ---------------------------------------------------------- the range
-    // Tiles before each sequence: every thread sums a slice of them.
-    const int slice = (p.B + C::kThreads - 1) / C::kThreads;
-    const int b_lo = min(p.B, tid * slice), b_hi = min(p.B, b_lo + slice);
+    // Steps before each sequence, in every warp by itself (no block barrier
+    // stands before the first load): a lane sums a slice of the sequences.
+    const int slice = (p.B + 31) >> 5;
+    const int b_lo = min(p.B, lane * slice), b_hi = min(p.B, b_lo + slice);
     int64_t mine = 0;
-    for (int b = b_lo; b < b_hi; ++b) mine += tiles_of<C::kKeys>(seq_len(p, b));
+    int b_len = 0;                                           // of the slice's last sequence
+    for (int b = b_lo; b < b_hi; ++b) {
+        b_len = seq_len(p, b);
+        mine += steps_of<C::kStep>(b_len);
+    }
     int64_t incl = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const int64_t up = __shfl_up_sync(0xffffffffu, incl, off);
         if (lane >= off) incl += up;
     }
-    if (lane == 31) s_scan[warp] = incl;
-    __syncthreads();
-    int64_t before = incl - mine, total = 0;
-#pragma unroll
-    for (int w = 0; w < C::kWarps; ++w) {
-        if (w < warp) before += s_scan[w];
-        total += s_scan[w];
-    }
-    const int64_t all = total * units;
-    // with fewer tiles than blocks, the first `busy` blocks take one each: a
-    // unit's parts then lie in consecutive blocks, none of them empty
-    const int64_t busy = min(all, (int64_t)kPdBlocks);
-    if ((int64_t)blockIdx.x >= busy) return;                 // uniform in the block
-    const int64_t t_lo = (int64_t)blockIdx.x * all / busy;
-    const int64_t t_hi = (int64_t)(blockIdx.x + 1) * all / busy;
-    const int64_t seq_tile = t_lo / units;                   // in tiles of one unit per sequence
-    if (before <= seq_tile && seq_tile < before + mine) {    // one thread
-        int b = b_lo;
-        for (;; ++b) {
-            const int n = tiles_of<C::kKeys>(seq_len(p, b));
-            if (seq_tile < before + n) break;
-            before += n;
+    const int64_t all = __shfl_sync(0xffffffffu, incl, 31) * units;
+    // With fewer steps than warps, the first `busy` warps take one step each,
+    // spread over the blocks: a unit's parts then lie in consecutive workers,
+    // none of them without work.
+    const int per = (int)min((int64_t)C::kWarps, div_pos(all + kPdBlocks - 1, kPdBlocks));
+    const int busy = (int)min(all, (int64_t)kPdBlocks * per);
+    if ((int)blockIdx.x * per >= busy) return;               // uniform in the block
+    const int worker = (int)blockIdx.x * per + warp;
+    const bool works = warp < per && worker < busy;
+    const int64_t quota = div_pos(all, busy), extra = all - quota * busy;
+    const int64_t count = works ? quota + (worker < extra ? 1 : 0) : 0;
+    const int64_t t_lo = worker * quota + min((int64_t)worker, extra);
+    PdCursor cur{};
+    if (works) {                                             // uniform in the warp
+        const int64_t want = div_pos(t_lo, units);           // in steps of one unit a sequence
+        int64_t at = incl - mine;
+        const bool owner = at <= want && want < incl;        // one lane
+        int b = b_lo, n = 1;
+        if (owner) {
+            if (slice > 1)
+                for (;; ++b) {
+                    b_len = seq_len(p, b);
+                    if (want < at + steps_of<C::kStep>(b_len)) break;
+                    at += steps_of<C::kStep>(b_len);
+                }
+            n = steps_of<C::kStep>(b_len);
         }
-        s_b = b;
-        s_at = before;
+        const int who = __ffs(__ballot_sync(0xffffffffu, owner)) - 1;
+        cur.b = __shfl_sync(0xffffffffu, b, who);
+        cur.len = __shfl_sync(0xffffffffu, b_len, who);
+        cur.n = __shfl_sync(0xffffffffu, n, who);
+        const int64_t in_seq = t_lo - __shfl_sync(0xffffffffu, at, who) * units;
+        cur.unit = (int)div_pos(in_seq, cur.n);
+        cur.step = (int)(in_seq - (int64_t)cur.unit * cur.n);
     }
-    __syncthreads();
-    PdCursor cur;
-    cur.b = s_b;
-    cur.len = seq_len(p, cur.b);
-    cur.n = tiles_of<C::kKeys>(cur.len);
-    int64_t unit_start;                                      // line index of the unit's tile 0
-    {
-        const int64_t in_seq = t_lo - s_at * units;
-        cur.unit = (int)(in_seq / cur.n);
-        cur.tile = (int)(in_seq - (int64_t)cur.unit * cur.n);
-        unit_start = t_lo - cur.tile;
-    }
-    const int64_t count = t_hi - t_lo;
 
     // ---------------------------------------------------------- loading
     const uint32_t ring = smem_u32(smem) + (uint32_t)(warp * C::kStages * C::kStage);
     uint32_t* my_seen = seen + warp * C::kStages;
     PdCursor put = cur;
     int64_t put_i = 0;
-    int entry = -1;                                          // page of this lane's next key
+    int64_t put_head = (put.unit / p.hblk) * p.c_sh;         // of the unit's K/V head
+    // A lane looks up one key of the next step: its own, or, where pages hold
+    // whole groups of 16 keys, the first of its group.
+    const int lane_key = p.whole16 ? lane & (C::kStep - 16) : lane & (C::kStep - 1);
+    int entry = -1, slot_in_page = 0;
     auto lookup = [&]() {
-        const int key = put.tile * C::kKeys + warp * 16 + (lane & 15);
+        const int key = put.step * C::kStep + lane_key;
+        const int pg = (int)(__umulhi(2u * (uint32_t)key, p.page_mul) >> p.page_shift);
+        slot_in_page = key - pg * p.page_size;
         entry = -1;
-        if (put_i < count && key < put.len)
-            entry = p.table[put.b * p.table_stride + key / p.page_size];
+        if (put_i < count && key < put.len) entry = p.table[put.b * p.table_stride + pg];
     };
     constexpr int kChunks = C::kRow / 16;                    // of a row
     constexpr int kRowsAt = 32 / kChunks;                    // rows of one warp-wide copy
+    const int my_row = lane / kChunks, my_chunk = lane % kChunks;
+    const int64_t lane_off = my_row * p.c_st + my_chunk * 16;
+    const int64_t v_off = p.vc - p.kc;
     auto issue = [&](int slot) {
         if (put_i < count) {
-            const int key = put.tile * C::kKeys + warp * 16 + (lane & 15);
             const bool ok = entry >= 0 && entry < p.num_pages;
-            const int64_t off = ok ? entry * p.c_sp + (put.unit / p.hblk) * p.c_sh +
-                                         (key % p.page_size) * p.c_st
-                                   : 0;
-            const uint32_t mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;
-            if (lane == 0) my_seen[slot] = mask;
-            if (mask != 0) {
-                const uint32_t kd = ring + (uint32_t)(slot * C::kStage), vd = kd + 16 * C::kRow;
-                const int c = lane % kChunks;
+            const int64_t off =
+                ok ? entry * p.c_sp + put_head + slot_in_page * p.c_st : 0;
+            const uint32_t kd = ring + (uint32_t)(slot * C::kStage), vd = kd + C::kStep * C::kRow;
+            uint32_t mask;
+            if (p.whole16) {
+                // the group's visible keys are its first ones
+                const int left = put.len - (put.step * C::kStep + lane_key);
+                const uint32_t mine16 = ok ? (left >= 16 ? 0xffffu : (1u << left) - 1u) : 0u;
+                mask = mine16;
+                if constexpr (C::kGroups == 2)
+                    mask = __shfl_sync(0xffffffffu, mine16, 0) |
+                           (__shfl_sync(0xffffffffu, mine16, 16) << 16);
+                if (mask != 0) {
 #pragma unroll
-                for (int i = 0; i < 16 / kRowsAt; ++i) {
-                    const int r = i * kRowsAt + lane / kChunks;
-                    const int64_t ro = __shfl_sync(0xffffffffu, off, r) + c * 16;
-                    const bool in = (mask >> r) & 1u;
-                    const uint32_t at = stage_at<C::kRow>(r, c);
-                    cp_async16(kd + at, p.kc + ro, in);
-                    cp_async16(vd + at, p.vc + ro, in);
+                    for (int g = 0; g < C::kGroups; ++g) {
+                        const uint8_t* src = p.kc + lane_off + __shfl_sync(0xffffffffu, off, g * 16);
+#pragma unroll
+                        for (int i = 0; i < 16 / kRowsAt; ++i) {
+                            const int r = g * 16 + i * kRowsAt + my_row;
+                            const bool in = (mask >> r) & 1u;
+                            const uint32_t at = stage_at<C::kRow>(r, my_chunk);
+                            const uint8_t* from = in ? src : p.kc;
+                            cp_async16(kd + at, from, in);
+                            cp_async16(vd + at, from + v_off, in);
+                            src += kRowsAt * p.c_st;
+                        }
+                    }
+                }
+            } else {
+                mask = __ballot_sync(0xffffffffu, ok);
+                if constexpr (C::kGroups == 1) mask &= 0xffffu;
+                if (mask != 0) {
+                    const uint8_t* base = p.kc + my_chunk * 16;
+#pragma unroll
+                    for (int i = 0; i < C::kStep / kRowsAt; ++i) {
+                        const int r = i * kRowsAt + my_row;
+                        const bool in = (mask >> r) & 1u;
+                        const uint8_t* from =
+                            (in ? base : p.kc) + __shfl_sync(0xffffffffu, off, r);
+                        const uint32_t at = stage_at<C::kRow>(r, my_chunk);
+                        cp_async16(kd + at, from, in);
+                        cp_async16(vd + at, from + v_off, in);
+                    }
                 }
             }
+            if (lane == 0) my_seen[slot] = mask;
             ++put_i;
-            pd_next<C::kKeys>(p, put, units);
+            const int was = put.unit;
+            pd_next<C::kStep>(p, put, units);
+            if (put.unit != was) put_head = (put.unit / p.hblk) * p.c_sh;
             lookup();
         }
         cp_async_commit();
@@ -364,65 +420,70 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
                 for (int j = 0; j < 4; ++j) o[mt][nt][j] = 0.f;
         }
     };
-    bool from_start = cur.tile == 0;                         // this block has the unit's tile 0
-    begin_unit();
+    bool from_start = cur.step == 0;                         // this warp has the unit's step 0
+    if (works) begin_unit();
 
-    // ---------------------------------------------------------- one stage
+    // ---------------------------------------------------------- one step
     const int kr = lane & 15, kcol = lane >> 4;              // ldmatrix rows: K
     const int vg = lane >> 3, vi = lane & 7;                 // and V (transposed)
     auto compute = [&](int slot) {
         const uint32_t mask = my_seen[slot];
         if (mask == 0) return;
-        const uint32_t kb = ring + (uint32_t)(slot * C::kStage), vb = kb + 16 * C::kRow;
-        float s[2][NT][4];
+        const uint32_t kb = ring + (uint32_t)(slot * C::kStage), vb = kb + C::kStep * C::kRow;
+        float x[C::kGroups][NT][4];
+        bool move = false;
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int g = 0; g < C::kGroups; ++g) {
+            float s[2][NT][4];                               // two chains of products
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[h][nt][j] = 0.f;
+            if constexpr (E == 2) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    uint32_t a[4];
+                    ldsm4(kb + stage_at<C::kRow>(g * 16 + kr, kk * 2 + kcol), a);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma16816<E>(s[kk & 1][nt], a, qf[kk][nt][0], qf[kk][nt][1]);
+                }
+            } else {
+#pragma unroll
+                for (int k2 = 0; k2 < D / 32; ++k2) {
+                    uint32_t r[4];
+                    ldsm4(kb + stage_at<C::kRow>(g * 16 + kr, k2 * 2 + kcol), r);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t a[4];
+                        widen_e4m3(r[2 * h], a[0], a[2]);
+                        widen_e4m3(r[2 * h + 1], a[1], a[3]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma16816<E>(s[h][nt], a, qf[2 * k2 + h][nt][0], qf[2 * k2 + h][nt][1]);
+                    }
+                }
+            }
+            const bool in0 = (mask >> (g * 16 + qr)) & 1u, in1 = (mask >> (g * 16 + qr + 8)) & 1u;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) s[h][nt][j] = 0.f;
-        if constexpr (E == 2) {
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                uint32_t a[4];
-                ldsm4(kb + stage_at<C::kRow>(kr, kk * 2 + kcol), a);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    mma16816<E>(s[kk & 1][nt], a, qf[kk][nt][0], qf[kk][nt][1]);
-            }
-        } else {
-#pragma unroll
-            for (int k2 = 0; k2 < D / 32; ++k2) {
-                uint32_t r[4];
-                ldsm4(kb + stage_at<C::kRow>(kr, k2 * 2 + kcol), r);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t a[4];
-                    widen_e4m3(r[2 * h], a[0], a[2]);
-                    widen_e4m3(r[2 * h + 1], a[1], a[3]);
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        mma16816<E>(s[h][nt], a, qf[2 * k2 + h][nt][0], qf[2 * k2 + h][nt][1]);
+                for (int j = 0; j < 4; ++j) {
+                    const float v = (s[0][nt][j] + s[1][nt][j]) * sc[nt][j & 1];
+                    x[g][nt][j] = (j < 2 ? in0 : in1) ? v : -INFINITY;
+                    move |= x[g][nt][j] > m[nt][j & 1] + 8.f;
                 }
-            }
         }
-        const bool in0 = (mask >> qr) & 1u, in1 = (mask >> (qr + 8)) & 1u;
-        float x[NT][4];
-        bool move = false;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const float v = (s[0][nt][j] + s[1][nt][j]) * sc[nt][j & 1];
-                x[nt][j] = (j < 2 ? in0 : in1) ? v : -INFINITY;
-                move |= x[nt][j] > m[nt][j & 1] + 8.f;
-            }
         if (__any_sync(0xffffffffu, move)) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    float t = fmaxf(x[nt][j], x[nt][j + 2]);
+                    float t = fmaxf(x[0][nt][j], x[0][nt][j + 2]);
+                    if constexpr (C::kGroups == 2)
+                        t = fmaxf(t, fmaxf(x[C::kGroups - 1][nt][j], x[C::kGroups - 1][nt][j + 2]));
                     t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 4));
                     t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 8));
                     t = fmaxf(t, __shfl_xor_sync(0xffffffffu, t, 16));
@@ -438,14 +499,16 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
                     }
                 }
         }
-        uint32_t pb[NT][2];
+        uint32_t pb[C::kGroups][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
             const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {                    // keys qr, then qr + 8
-                const float p0 = fast_exp2(x[nt][2 * h] - m0), p1 = fast_exp2(x[nt][2 * h + 1] - m1);
+            for (int gh = 0; gh < 2 * C::kGroups; ++gh) {    // keys qr, then qr + 8, of a group
+                const int g = gh >> 1, h = gh & 1;
+                const float p0 = fast_exp2(x[g][nt][2 * h] - m0);
+                const float p1 = fast_exp2(x[g][nt][2 * h + 1] - m1);
                 l[nt][0] += p0;
                 l[nt][1] += p1;
                 uint32_t u;
@@ -459,157 +522,125 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
                     lr[nt][0] += f.x;
                     lr[nt][1] += f.y;
                 }
-                pb[nt][h] = transpose8x8(u);
+                pb[g][nt][h] = transpose8x8(u);
             }
         }
-        if constexpr (E == 2) {
 #pragma unroll
-            for (int mt = 0; mt < D / 16; ++mt) {
-                uint32_t a[4];
-                ldsm4_t(vb + stage_at<C::kRow>((vg >> 1) * 8 + vi, 2 * mt + (vg & 1)), a);
+        for (int g = 0; g < C::kGroups; ++g) {
+            if constexpr (E == 2) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) mma16816<E>(o[mt][nt], a, pb[nt][0], pb[nt][1]);
-            }
-        } else {
-            // a transposed 16-bit block gives, for head-dim pair 2 qr, 2 qr + 1
-            // (bytes) and keys 2 qc, 2 qc + 1: rows qr and qr + 8 of the
-            // product's A are head dims 2 qr and 2 qr + 1
-#pragma unroll
-            for (int m2 = 0; m2 < D / 32; ++m2) {
-                uint32_t r[4];
-                ldsm4_t(vb + stage_at<C::kRow>((vg & 1) * 8 + vi, 2 * m2 + (vg >> 1)), r);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
+                for (int mt = 0; mt < D / 16; ++mt) {
                     uint32_t a[4];
-                    widen_e4m3(__byte_perm(r[2 * h], 0u, 0x3120), a[0], a[1]);
-                    widen_e4m3(__byte_perm(r[2 * h + 1], 0u, 0x3120), a[2], a[3]);
+                    ldsm4_t(vb + stage_at<C::kRow>(g * 16 + (vg >> 1) * 8 + vi, 2 * mt + (vg & 1)), a);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
-                        mma16816<E>(o[2 * m2 + h][nt], a, pb[nt][0], pb[nt][1]);
+                        mma16816<E>(o[mt][nt], a, pb[g][nt][0], pb[g][nt][1]);
+                }
+            } else {
+                // a transposed 16-bit block gives, for head-dim pair 2 qr, 2 qr + 1
+                // (bytes) and keys 2 qc, 2 qc + 1: rows qr and qr + 8 of the
+                // product's A are head dims 2 qr and 2 qr + 1
+#pragma unroll
+                for (int m2 = 0; m2 < D / 32; ++m2) {
+                    uint32_t r[4];
+                    ldsm4_t(vb + stage_at<C::kRow>(g * 16 + (vg & 1) * 8 + vi, 2 * m2 + (vg >> 1)), r);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t a[4];
+                        widen_e4m3(__byte_perm(r[2 * h], 0u, 0x3120), a[0], a[1]);
+                        widen_e4m3(__byte_perm(r[2 * h + 1], 0u, 0x3120), a[2], a[3]);
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            mma16816<E>(o[2 * m2 + h][nt], a, pb[g][nt][0], pb[g][nt][1]);
+                    }
                 }
             }
         }
     };
 
-    // ---------------------------------------------------------- end of a unit's part
-    auto end_unit = [&](bool to_end, int64_t line) {
-        // per-warp statistics, then the common reference of the block
+    // ---------------------------------------------------------- a unit's end in this warp
+    auto add_lanes = [&]() {                                 // sums over the 8 lanes of a column
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
+            for (int j = 0; j < 2; ++j)
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) {
                     l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], off);
                     lr[nt][j] += __shfl_xor_sync(0xffffffffu, lr[nt][j], off);
                 }
-                if (qr == 0) {
-                    const int h = warp * C::kHeads + nt * 8 + 2 * qc + j;
-                    st_m[h] = m[nt][j];
-                    st_l[h] = l[nt][j];
-                    st_lr[h] = lr[nt][j];
+    };
+    // log2-sum-exp of exact sum `sum` with reference m: -inf for no key at all
+    auto lse2 = [](float sum, float ref) {
+        return sum == 0.f ? -INFINITY : (ref == -INFINITY ? 0.f : ref) + log2f(sum);
+    };
+    auto end_unit = [&]() {
+        add_lanes();
+        const int hkv = cur.unit / p.hblk, hb = cur.unit - hkv * p.hblk;
+        if (from_start) {
+            if (lane == 0) p.split[(int64_t)cur.b * units + cur.unit] = make_int2(-1, -1);
+            const int64_t row0 = (int64_t)cur.b * p.H + hkv * p.G + hb * C::kHeads;
+            const int heads = p.G - hb * C::kHeads;          // live ones of this block of heads
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float inv[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    inv[j] = lr[nt][j] == 0.f ? 0.f : p.o_mul / lr[nt][j];   // no visible key: 0
+                    const int h = nt * 8 + 2 * qc + j;
+                    if (qr == 0 && h < heads)
+                        p.lse[row0 + h] = lse2(l[nt][j], m[nt][j]) * 0.6931471805599453f;
+                }
+#pragma unroll
+                for (int mt = 0; mt < D / 16; ++mt) {
+                    const float(&f)[4] = o[mt][nt];
+                    if constexpr (E == 2) {
+                        // 8 x 8 blocks transposed: head qr, two neighbouring columns
+#pragma unroll
+                        for (int h8 = 0; h8 < 2; ++h8) {
+                            const uint32_t u = transpose8x8(
+                                pack_bf16x2(f[2 * h8] * inv[0], f[2 * h8 + 1] * inv[1]));
+                            if (nt * 8 + qr < heads)
+                                *reinterpret_cast<uint32_t*>(p.o + (row0 + nt * 8 + qr) * D +
+                                                             mt * 16 + h8 * 8 + 2 * qc) = u;
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                            if (nt * 8 + 2 * qc + j < heads)
+                                *reinterpret_cast<uint32_t*>(
+                                    p.o + (row0 + nt * 8 + 2 * qc + j) * D + mt * 16 + 2 * qr) =
+                                    pack_bf16x2(f[j] * inv[j], f[j + 2] * inv[j]);
+                    }
                 }
             }
-        __syncthreads();
-        const bool whole = from_start && to_end;
-        const int hkv = cur.unit / p.hblk, hb = cur.unit - hkv * p.hblk;
-        const int64_t slot = (int64_t)blockIdx.x * 2 + (from_start ? 1 : 0);
-        if (tid == 0 && from_start) {
-            int2 sp = make_int2(-1, -1);
-            if (!to_end) {
-                const int64_t last = line + (cur.n - 1 - cur.tile);       // the unit's last tile
-                sp = make_int2((int)blockIdx.x, (int)(((last + 1) * busy - 1) / all));
-            }
-            p.split[(int64_t)cur.b * units + cur.unit] = sp;
-        }
-        auto reference = [&](int h) {
-            float r = -INFINITY;
+        } else {
+            const int64_t row0 = ((int64_t)blockIdx.x * 2 * C::kWarps + warp) * C::kHeads;
 #pragma unroll
-            for (int w = 0; w < C::kWarps; ++w) r = fmaxf(r, st_m[w * C::kHeads + h]);
-            return r;
-        };
-        auto weighted = [&](const float* st, int h, float ref) {
-            float t = 0.f;
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int w = 0; w < C::kWarps; ++w) {
-                const float mw = st_m[w * C::kHeads + h];
-                // a warp without a finite score has sums of 0, or NaN to pass on
-                t += (mw == -INFINITY ? 1.f : fast_exp2(mw - ref)) * st[w * C::kHeads + h];
-            }
-            return t;
-        };
+                for (int j = 0; j < 2; ++j) {
+                    const int64_t row = row0 + nt * 8 + 2 * qc + j;
+                    const float inv = lr[nt][j] == 0.f ? 0.f : p.o_mul / lr[nt][j];
+                    if (qr == 0) p.part_lse[row] = lse2(l[nt][j], m[nt][j]);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            float a[2];
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                const float ref = reference(nt * 8 + 2 * qc + j);
-                a[j] = m[nt][j] == -INFINITY ? 0.f : fast_exp2(m[nt][j] - ref);
-            }
-#pragma unroll
-            for (int d0 = 0; d0 < D; d0 += C::kCols) {
-                float* mine_m = merge + warp * 8 * kPdPitch;
-#pragma unroll
-                for (int t = 0; t < C::kCols / 16; ++t) {
-                    const int mt = d0 / 16 + t;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        float* row = mine_m + (2 * qc + j) * kPdPitch + t * 16;
+                    for (int mt = 0; mt < D / 16; ++mt) {
+                        float* dst = p.part_o + row * D + mt * 16;
                         if constexpr (E == 2) {
-                            row[qr] = o[mt][nt][j] * a[j];
-                            row[qr + 8] = o[mt][nt][j + 2] * a[j];
+                            dst[qr] = o[mt][nt][j] * inv;
+                            dst[qr + 8] = o[mt][nt][j + 2] * inv;
                         } else {
-                            *reinterpret_cast<float2*>(row + 2 * qr) =
-                                make_float2(o[mt][nt][j] * a[j], o[mt][nt][j + 2] * a[j]);
+                            *reinterpret_cast<float2*>(dst + 2 * qr) =
+                                make_float2(o[mt][nt][j] * inv, o[mt][nt][j + 2] * inv);
                         }
                     }
                 }
-                __syncthreads();
-                for (int e = tid; e < 8 * C::kCols / 4; e += C::kThreads) {
-                    const int hh = e / (C::kCols / 4), col = (e - hh * (C::kCols / 4)) * 4;
-                    const int h = nt * 8 + hh, g = hb * C::kHeads + h;
-                    if (g >= p.G) continue;
-                    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int w = 0; w < C::kWarps; ++w) {
-                        const float4 v = *reinterpret_cast<const float4*>(
-                            merge + (w * 8 + hh) * kPdPitch + col);
-                        t.x += v.x;
-                        t.y += v.y;
-                        t.z += v.z;
-                        t.w += v.w;
-                    }
-                    const float ref = reference(h);
-                    const float sum = weighted(st_lr, h, ref);
-                    const float inv = sum == 0.f ? 0.f : p.o_mul / sum;   // no visible key: 0
-                    t.x *= inv;
-                    t.y *= inv;
-                    t.z *= inv;
-                    t.w *= inv;
-                    const bool stat = d0 == 0 && col == 0;
-                    float ls = -INFINITY;
-                    if (stat) {
-                        const float exact = weighted(st_l, h, ref);
-                        if (exact != 0.f) ls = (ref == -INFINITY ? 0.f : ref) + log2f(exact);
-                    }
-                    if (whole) {
-                        const int64_t row = (int64_t)cur.b * p.H + hkv * p.G + g;
-                        *reinterpret_cast<uint2*>(p.o + row * D + d0 + col) =
-                            make_uint2(pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w));
-                        if (stat) p.lse[row] = ls * 0.6931471805599453f;
-                    } else {
-                        const int64_t row = slot * C::kHeads + h;
-                        *reinterpret_cast<float4*>(p.part_o + row * D + d0 + col) = t;
-                        if (stat) p.part_lse[row] = ls;
-                    }
-                }
-                __syncthreads();                             // the buffer is free again
-            }
         }
     };
 
     // ---------------------------------------------------------- the loop
     int get = 0, fill = C::kStages - 1;
+    bool open = false;                                       // inside a unit at the range's end
     for (int64_t i = 0; i < count; ++i) {
         cp_async_wait<C::kStages - 2>();
         __syncwarp();           // stage `get` is in, and every lane is done with stage `fill`
@@ -617,75 +648,211 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
         compute(get);
         get = get + 1 == C::kStages ? 0 : get + 1;
         fill = fill + 1 == C::kStages ? 0 : fill + 1;
-        const bool last_tile = cur.tile + 1 == cur.n;
-        if (last_tile || i + 1 == count) {
-            end_unit(last_tile, t_lo + i);
+        if (cur.step + 1 == cur.n) {
+            end_unit();
             from_start = true;
             if (i + 1 < count) {
-                pd_next<C::kKeys>(p, cur, units);
+                pd_next<C::kStep>(p, cur, units);
                 begin_unit();
             }
+        } else if (i + 1 < count) {
+            ++cur.step;
         } else {
-            ++cur.tile;
+            open = true;
         }
     }
     cp_async_wait<0>();
+
+    // ---------------------------------------------------------- parts of open units
+    if (open) {
+        add_lanes();
+        if (qr == 0) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int h = warp * C::kHeads + nt * 8 + 2 * qc + j;
+                    st_m[h] = m[nt][j];
+                    st_l[h] = l[nt][j];
+                    st_lr[h] = lr[nt][j];
+                }
+        }
+        if (lane == 0 && from_start) {
+            // the unit's last step, and the warp that has it
+            const int64_t last = t_lo + count - 1 + (cur.n - 1 - cur.step);
+            const int64_t wide = extra * (quota + 1);        // steps of the longer ranges
+            const int end = (int)(last < wide ? div_pos(last, quota + 1)
+                                              : extra + div_pos(last - wide, quota));
+            p.split[(int64_t)cur.b * units + cur.unit] =
+                make_int2((int)blockIdx.x * C::kWarps + warp,
+                          end / per * C::kWarps + end % per);
+        }
+    }
+    if (lane == 0) s_open[warp] = open ? (int64_t)cur.b * units + cur.unit : -1;
+    __syncthreads();                                         // rings are done with, too
+    // Warps that follow one another inside one unit form a group; its common
+    // reference is the largest of theirs.
+    int first = warp, past = warp + 1;
+    if (open) {
+        while (first > 0 && s_open[first - 1] == s_open[warp]) --first;
+        while (past < C::kWarps && s_open[past] == s_open[warp]) ++past;
+        float* mine_o = reinterpret_cast<float*>(smem) + warp * C::kHeads * C::kPitch;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int h = nt * 8 + 2 * qc + j;
+                float ref = -INFINITY;
+                for (int w = first; w < past; ++w) ref = fmaxf(ref, st_m[w * C::kHeads + h]);
+                const float a = m[nt][j] == -INFINITY ? 0.f : fast_exp2(m[nt][j] - ref);
+#pragma unroll
+                for (int mt = 0; mt < D / 16; ++mt) {
+                    float* row = mine_o + h * C::kPitch + mt * 16;
+                    if constexpr (E == 2) {
+                        row[qr] = o[mt][nt][j] * a;
+                        row[qr + 8] = o[mt][nt][j + 2] * a;
+                    } else {
+                        *reinterpret_cast<float2*>(row + 2 * qr) =
+                            make_float2(o[mt][nt][j] * a, o[mt][nt][j + 2] * a);
+                    }
+                }
+            }
+    }
+    __syncthreads();
+    for (int w0 = 0; w0 < C::kWarps;) {
+        const int64_t unit = s_open[w0];
+        int w1 = w0 + 1;
+        while (w1 < C::kWarps && s_open[w1] == unit) ++w1;
+        if (unit >= 0) {
+            const int64_t row0 = ((int64_t)(blockIdx.x * 2 + 1) * C::kWarps + w0) * C::kHeads;
+            for (int e = tid; e < C::kHeads * (D / 4); e += C::kThreads) {
+                const int h = e / (D / 4), col = (e - h * (D / 4)) * 4;
+                float ref = -INFINITY, sum = 0.f, exact = 0.f;
+                for (int w = w0; w < w1; ++w) ref = fmaxf(ref, st_m[w * C::kHeads + h]);
+                float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int w = w0; w < w1; ++w) {
+                    const int sh = w * C::kHeads + h;
+                    // a warp without a finite score has sums of 0, or NaN to pass on
+                    const float a = st_m[sh] == -INFINITY ? 1.f : fast_exp2(st_m[sh] - ref);
+                    sum += a * st_lr[sh];
+                    exact += a * st_l[sh];
+                    const float4 v = *reinterpret_cast<const float4*>(
+                        reinterpret_cast<const float*>(smem) + sh * C::kPitch + col);
+                    t.x += v.x;
+                    t.y += v.y;
+                    t.z += v.z;
+                    t.w += v.w;
+                }
+                const float inv = sum == 0.f ? 0.f : p.o_mul / sum;
+                *reinterpret_cast<float4*>(p.part_o + (row0 + h) * D + col) =
+                    make_float4(t.x * inv, t.y * inv, t.z * inv, t.w * inv);
+                if (col == 0) p.part_lse[row0 + h] = lse2(exact, ref);
+            }
+        }
+        w0 = w1;
+    }
 }
 
-// Joins the parts of the units that more than one block worked on: one warp a
-// row (sequence, query head), D / 32 columns a lane, parts in block order.
-constexpr int kPdJoinWarps = 4;
+// Joins the parts of the units that more than one warp worked on: one block a
+// row (sequence, query head), D / 4 lanes (a float4 each) a part, parts in the
+// order of the keys: one of each block that the unit does not end in, one of
+// the block that it ends in unless it ends in the first warp inside it there,
+// and the last. It is all latency (a row has some 20 parts at most), so the
+// parts are spread over the block's lanes and their loads do not wait for the
+// log-sum-exps: with one warp a row, parts one after another, it took 8 us of
+// the 95 of a 131072-key sequence; so, @JOIN@.
+constexpr int kPdJoinThreads = 256;
 
 template <int D>
-__global__ void __launch_bounds__(32 * kPdJoinWarps)
-    fa_paged_join(const PdParams p, int heads) {
+__global__ void __launch_bounds__(kPdJoinThreads)
+    fa_paged_join(const PdParams p, int heads, int warps) {
     pdl_wait_prerequisites();
-    constexpr int kPer = D / 32;
-    const int64_t row = (int64_t)blockIdx.x * kPdJoinWarps + (threadIdx.x >> 5);
-    const int lane = threadIdx.x & 31;
-    if (row >= (int64_t)p.B * p.H) return;
+    constexpr int kLanes = D / 4;                            // of a part
+    constexpr int kAt = kPdJoinThreads / kLanes;             // parts at once
+    constexpr int kMost = 4;                                 // kept in registers a lane
+    __shared__ float4 s_acc[kPdJoinThreads];
+    __shared__ float s_m[kAt], s_w[kAt];
+    const int64_t row = blockIdx.x;
     const int b = (int)(row / p.H), h = (int)(row - (int64_t)b * p.H);
     const int hkv = h / p.G, g = h - hkv * p.G, hb = g / heads;
     const int2 sp = p.split[((int64_t)b * p.H_kv + hkv) * p.hblk + hb];
     if (sp.x < 0) return;
-    const int hh = g - hb * heads, parts = sp.y - sp.x + 1;
-    // part i: block sp.x + i, whose first part of the two it is unless the
-    // unit began there
-    auto at = [&](int i) { return ((int64_t)(sp.x + i) * 2 + (i == 0 ? 1 : 0)) * heads + hh; };
-    float mx = -INFINITY;
-    for (int i = lane; i < parts; i += 32) mx = fmaxf(mx, p.part_lse[at(i)]);
+    const int hh = g - hb * heads;
+    const int blk0 = sp.x / warps, w0 = sp.x - blk0 * warps;
+    const int blk1 = sp.y / warps, w1 = sp.y - blk1 * warps;
+    const int inside = blk1 - blk0 + (w1 > (blk0 == blk1 ? w0 : 0) ? 1 : 0);
+    const int parts = inside + 1;
+    auto at = [&](int i) {
+        const int slot = i < inside ? ((blk0 + i) * 2 + 1) * warps + (i == 0 ? w0 : 0)
+                                    : blk1 * 2 * warps + w1;
+        return slot * heads + hh;
+    };
+    const int mine = (int)threadIdx.x / kLanes, c = (int)threadIdx.x % kLanes;
+    float m = -INFINITY, wsum = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int i0 = mine; i0 < parts; i0 += kAt * kMost) {
+        float ls[kMost];
+        float4 v[kMost];
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-    float acc[kPer], wsum = 0.f;
-#pragma unroll
-    for (int c = 0; c < kPer; ++c) acc[c] = 0.f;
-    if (mx == -INFINITY) mx = 0.f;                           // no finite part: zeros, or NaN
-    for (int i0 = 0; i0 < parts; i0 += 32) {
-        const float ls = i0 + lane < parts ? p.part_lse[at(i0 + lane)] : -INFINITY;
-        const float wl = ls == -INFINITY ? 0.f : exp2f(ls - mx);
-        wsum += wl;
-        const int cnt = min(32, parts - i0);
-#pragma unroll 4
-        for (int i = 0; i < cnt; ++i) {
-            const float w = __shfl_sync(0xffffffffu, wl, i);
-            const float* src = p.part_o + at(i0 + i) * D + lane * kPer;
-#pragma unroll
-            for (int c = 0; c < kPer; c += 2) {
-                const float2 v = *reinterpret_cast<const float2*>(src + c);
-                acc[c] = fmaf(w, v.x, acc[c]);
-                acc[c + 1] = fmaf(w, v.y, acc[c + 1]);
+        for (int u = 0; u < kMost; ++u) {
+            const int i = i0 + u * kAt;
+            ls[u] = -INFINITY;
+            if (i < parts) {
+                const int r = at(i);
+                ls[u] = p.part_lse[r];
+                v[u] = *reinterpret_cast<const float4*>(p.part_o + (int64_t)r * D + c * 4);
             }
         }
+        float mx = m;
+#pragma unroll
+        for (int u = 0; u < kMost; ++u) mx = fmaxf(mx, ls[u]);
+        const float ref = mx == -INFINITY ? 0.f : mx;        // no finite part: zeros, or NaN
+        const float keep = m == -INFINITY ? 1.f : exp2f(m - ref);
+        wsum *= keep;
+        acc.x *= keep;
+        acc.y *= keep;
+        acc.z *= keep;
+        acc.w *= keep;
+        m = mx;
+#pragma unroll
+        for (int u = 0; u < kMost; ++u) {
+            if (ls[u] == -INFINITY) continue;
+            const float w = exp2f(ls[u] - ref);
+            wsum += w;
+            acc.x = fmaf(w, v[u].x, acc.x);
+            acc.y = fmaf(w, v[u].y, acc.y);
+            acc.z = fmaf(w, v[u].z, acc.z);
+            acc.w = fmaf(w, v[u].w, acc.w);
+        }
     }
+    s_acc[threadIdx.x] = acc;
+    if (c == 0) {
+        s_m[mine] = m;
+        s_w[mine] = wsum;
+    }
+    __syncthreads();
+    if (mine != 0) return;
+    float mx = -INFINITY;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, off);
-    const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
+    for (int k = 0; k < kAt; ++k) mx = fmaxf(mx, s_m[k]);
+    const float ref = mx == -INFINITY ? 0.f : mx;
+    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
 #pragma unroll
-    for (int c = 0; c < kPer; c += 2)
-        *reinterpret_cast<uint32_t*>(p.o + row * D + lane * kPer + c) =
-            pack_bf16x2(acc[c] * inv, acc[c + 1] * inv);
-    if (lane == 0)
-        p.lse[row] = wsum == 0.f ? -INFINITY : (mx + log2f(wsum)) * 0.6931471805599453f;
+    for (int k = 0; k < kAt; ++k) {
+        const float w = s_m[k] == -INFINITY ? 1.f : exp2f(s_m[k] - ref);   // 1: of 0, or NaN
+        const float4 a = s_acc[k * kLanes + c];
+        sum = fmaf(w, s_w[k], sum);
+        t.x = fmaf(w, a.x, t.x);
+        t.y = fmaf(w, a.y, t.y);
+        t.z = fmaf(w, a.z, t.z);
+        t.w = fmaf(w, a.w, t.w);
+    }
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    *reinterpret_cast<uint2*>(p.o + row * D + c * 4) =
+        make_uint2(pack_bf16x2(t.x * inv, t.y * inv), pack_bf16x2(t.z * inv, t.w * inv));
+    if (c == 0)
+        p.lse[row] = sum == 0.f ? -INFINITY : (ref + log2f(sum)) * 0.6931471805599453f;
 }
 
 }  // namespace fa
