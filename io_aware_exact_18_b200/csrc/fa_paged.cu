@@ -166,6 +166,22 @@ PdPlan pd_plan(int B, int H, int H_kv, int d) {
     return pl;
 }
 
+template <int D, int kAt>
+int launch_join(const PdParams& p, int heads, int warps, cudaStream_t s) {
+    using C = PdJoinCfg<D, kAt>;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(((int64_t)p.B * p.H + C::kRows - 1) / C::kRows));
+    cfg.blockDim = dim3(C::kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fa_paged_join<D, kAt>, p, heads, warps);
+    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+}
+
 template <int D, int E, int NT>
 int launch_decode(const PdParams& p, cudaStream_t s) {
     using C = PdCfg<D, E, NT>;
@@ -182,18 +198,9 @@ int launch_decode(const PdParams& p, cudaStream_t s) {
     }
     kern<<<kPdBlocks, C::kThreads, C::kSmem, s>>>(p);
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_LAUNCH;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((int64_t)p.B * p.H));
-    cfg.blockDim = dim3(kPdJoinThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, fa_paged_join<D>, p, (int)C::kHeads,
-                                             (int)C::kWarps);
-    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+    if ((int64_t)p.B * p.H_kv * p.hblk >= kPdJoinUnits)
+        return launch_join<D, 1>(p, C::kHeads, C::kWarps, s);
+    return launch_join<D, 8>(p, C::kHeads, C::kWarps, s);
 }
 
 template <int D>

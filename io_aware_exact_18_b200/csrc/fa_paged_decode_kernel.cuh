@@ -349,46 +349,49 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
         }
         cp_async_commit();
     };
-    lookup();
-    for (int s = 0; s < C::kStages - 1; ++s) issue(s);
-
     // ---------------------------------------------------------- state
     uint32_t qf[D / 16][NT][2];
     float o[D / 16][NT][4];
     float m[NT][2], l[NT][2], lr[NT][2], sc[NT][2];
     const int qr = lane >> 2, qc = lane & 3;
-    auto begin_unit = [&]() {
+    // The unit's queries as they lie in memory: requested before the last
+    // unit's results are written, so that the two latencies overlap.
+    auto load_q = [&]() {
         const int hkv = cur.unit / p.hblk, hb = cur.unit - hkv * p.hblk;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const int g = hb * C::kHeads + nt * 8 + qr;      // head of the group
             const bool in = g < p.G;
             const __nv_bfloat16* src = p.q + cur.b * p.q_sb + (int64_t)(hkv * p.G + (in ? g : 0)) * p.q_sh;
-            if constexpr (E == 2) {
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk)
+            for (int kk = 0; kk < D / 16; ++kk) {
+                if constexpr (E == 2) {
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
                         qf[kk][nt][j] = in ? *reinterpret_cast<const uint32_t*>(
                                                  src + kk * 16 + j * 8 + 2 * qc) : 0u;
-                sc[nt][0] = sc[nt][1] = p.scale_log2;
-            } else {
-                // f16 q, scaled to a largest magnitude in [1, 2): element order
-                // 4 qc .. 4 qc + 3 of each 16, as the keys' bytes come
-                float amax = 0.f;
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
+                } else {                                     // 4 qc .. 4 qc + 3 of each 16,
                     const uint2 u = in ? *reinterpret_cast<const uint2*>(src + kk * 16 + 4 * qc)
-                                       : make_uint2(0u, 0u);
+                                       : make_uint2(0u, 0u); // as the keys' bytes come
                     qf[kk][nt][0] = u.x;
                     qf[kk][nt][1] = u.y;
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const uint32_t w = j ? u.y : u.x;
-                        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(w << 16)),
-                                                 fabsf(__uint_as_float(w & 0xffff0000u))));
-                    }
                 }
+            }
+        }
+    };
+    auto begin_unit = [&]() {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            sc[nt][0] = sc[nt][1] = p.scale_log2;
+            if constexpr (E == 1) {
+                // f16 q, scaled to a largest magnitude in [1, 2)
+                float amax = 0.f;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        amax = fmaxf(amax, fmaxf(fabsf(__uint_as_float(qf[kk][nt][j] << 16)),
+                                                 fabsf(__uint_as_float(qf[kk][nt][j] & 0xffff0000u))));
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
                 int ex = (int)(__float_as_uint(amax) >> 23) - 127;
@@ -421,6 +424,9 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
         }
     };
     bool from_start = cur.step == 0;                         // this warp has the unit's step 0
+    lookup();
+    if (works) load_q();
+    for (int s = 0; s < C::kStages - 1; ++s) issue(s);
     if (works) begin_unit();
 
     // ---------------------------------------------------------- one step
@@ -574,12 +580,14 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
     auto lse2 = [](float sum, float ref) {
         return sum == 0.f ? -INFINITY : (ref == -INFINITY ? 0.f : ref) + log2f(sum);
     };
-    auto end_unit = [&]() {
+    // whole: the unit's row; otherwise this warp's part, into slot kind (0: the
+    // unit ends here, 1: it goes on)
+    auto finish = [&](int b, int unit, bool whole, int kind) {
         add_lanes();
-        const int hkv = cur.unit / p.hblk, hb = cur.unit - hkv * p.hblk;
-        if (from_start) {
-            if (lane == 0) p.split[(int64_t)cur.b * units + cur.unit] = make_int2(-1, -1);
-            const int64_t row0 = (int64_t)cur.b * p.H + hkv * p.G + hb * C::kHeads;
+        const int hkv = unit / p.hblk, hb = unit - hkv * p.hblk;
+        if (whole) {
+            if (lane == 0) p.split[(int64_t)b * units + unit] = make_int2(-1, -1);
+            const int64_t row0 = (int64_t)b * p.H + hkv * p.G + hb * C::kHeads;
             const int heads = p.G - hb * C::kHeads;          // live ones of this block of heads
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -615,7 +623,8 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
                 }
             }
         } else {
-            const int64_t row0 = ((int64_t)blockIdx.x * 2 * C::kWarps + warp) * C::kHeads;
+            const int64_t row0 =
+                ((int64_t)(blockIdx.x * 2 + kind) * C::kWarps + warp) * C::kHeads;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -640,7 +649,7 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
 
     // ---------------------------------------------------------- the loop
     int get = 0, fill = C::kStages - 1;
-    bool open = false;                                       // inside a unit at the range's end
+    bool grouped = false;            // ends inside a unit that a neighbour is inside of, too
     for (int64_t i = 0; i < count; ++i) {
         cp_async_wait<C::kStages - 2>();
         __syncwarp();           // stage `get` is in, and every lane is done with stage `fill`
@@ -648,23 +657,41 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
         compute(get);
         get = get + 1 == C::kStages ? 0 : get + 1;
         fill = fill + 1 == C::kStages ? 0 : fill + 1;
-        if (cur.step + 1 == cur.n) {
-            end_unit();
-            from_start = true;
-            if (i + 1 < count) {
-                pd_next<C::kStep>(p, cur, units);
-                begin_unit();
-            }
-        } else if (i + 1 < count) {
+        const bool ends = cur.step + 1 == cur.n, more = i + 1 < count;
+        if (!ends && more) {
             ++cur.step;
-        } else {
-            open = true;
+            continue;
         }
+        const int b = cur.b, unit = cur.unit;
+        if (!ends) {
+            // The range ends inside the unit. The warp before it in the block
+            // is inside it unless it starts here; the one after it is unless
+            // it ends there.
+            const int64_t last = t_lo + i + (cur.n - 1 - cur.step);      // the unit's last step
+            const int64_t next_end = t_lo + count + quota + (worker + 1 < extra ? 1 : 0);
+            grouped = (!from_start && warp > 0) || (last >= next_end && warp + 1 < per);
+            if (lane == 0 && from_start) {                   // the warp that has the last step
+                const int64_t wide = extra * (quota + 1);    // steps of the longer ranges
+                const int end = (int)(last < wide ? div_pos(last, quota + 1)
+                                                  : extra + div_pos(last - wide, quota));
+                p.split[(int64_t)b * units + unit] =
+                    make_int2((int)blockIdx.x * C::kWarps + warp,
+                              end / per * C::kWarps + end % per);
+            }
+            if (grouped) break;
+        }
+        if (more) {
+            pd_next<C::kStep>(p, cur, units);
+            load_q();
+        }
+        finish(b, unit, ends && from_start, ends ? 0 : 1);
+        from_start = true;
+        if (more) begin_unit();
     }
     cp_async_wait<0>();
 
-    // ---------------------------------------------------------- parts of open units
-    if (open) {
+    // ---------------------------------------------------------- parts of groups
+    if (grouped) {
         add_lanes();
         if (qr == 0) {
 #pragma unroll
@@ -677,23 +704,13 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
                     st_lr[h] = lr[nt][j];
                 }
         }
-        if (lane == 0 && from_start) {
-            // the unit's last step, and the warp that has it
-            const int64_t last = t_lo + count - 1 + (cur.n - 1 - cur.step);
-            const int64_t wide = extra * (quota + 1);        // steps of the longer ranges
-            const int end = (int)(last < wide ? div_pos(last, quota + 1)
-                                              : extra + div_pos(last - wide, quota));
-            p.split[(int64_t)cur.b * units + cur.unit] =
-                make_int2((int)blockIdx.x * C::kWarps + warp,
-                          end / per * C::kWarps + end % per);
-        }
     }
-    if (lane == 0) s_open[warp] = open ? (int64_t)cur.b * units + cur.unit : -1;
-    __syncthreads();                                         // rings are done with, too
+    if (lane == 0) s_open[warp] = grouped ? (int64_t)cur.b * units + cur.unit : -1;
+    if (!__syncthreads_or(grouped)) return;                  // rings are done with, too
     // Warps that follow one another inside one unit form a group; its common
     // reference is the largest of theirs.
     int first = warp, past = warp + 1;
-    if (open) {
+    if (grouped) {
         while (first > 0 && s_open[first - 1] == s_open[warp]) --first;
         while (past < C::kWarps && s_open[past] == s_open[warp]) ++past;
         float* mine_o = reinterpret_cast<float*>(smem) + warp * C::kHeads * C::kPitch;
@@ -753,26 +770,36 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
     }
 }
 
-// Joins the parts of the units that more than one warp worked on: one block a
-// row (sequence, query head), D / 4 lanes (a float4 each) a part, parts in the
+// Joins the parts of the units that more than one warp worked on. Parts in the
 // order of the keys: one of each block that the unit does not end in, one of
 // the block that it ends in unless it ends in the first warp inside it there,
-// and the last. It is all latency (a row has some 20 parts at most), so the
-// parts are spread over the block's lanes and their loads do not wait for the
-// log-sum-exps: with one warp a row, parts one after another, it took 8 us of
-// the 95 of a 131072-key sequence; so, @JOIN@.
-constexpr int kPdJoinThreads = 256;
+// and the last. It is all latency, so a row (sequence, query head) has kAt
+// parts loaded side by side, D / 4 lanes (a float4 each) a part, and their
+// loads do not wait for the log-sum-exps. kAt = 8, a block a row, where units
+// are few and have many parts (up to one a block: with one warp a row, parts
+// one after another, the join took 8 us of the 95 of a 131072-key sequence;
+// so, @JOIN@); kAt = 1, rows side by side in a block, from kPdJoinUnits units
+// on, which have at most four parts on average (@JOIN1@).
+constexpr int kPdJoinUnits = 4 * kPdBlocks;
 
-template <int D>
-__global__ void __launch_bounds__(kPdJoinThreads)
+template <int D, int kAt>
+struct PdJoinCfg {
+    static constexpr int kLanes = D / 4;                     // of a part
+    static constexpr int kRows = kAt == 1 ? 128 / kLanes : 1;            // of a block
+    static constexpr int kThreads = kLanes * kAt * kRows;
+};
+
+template <int D, int kAt>
+__global__ void __launch_bounds__(PdJoinCfg<D, kAt>::kThreads)
     fa_paged_join(const PdParams p, int heads, int warps) {
     pdl_wait_prerequisites();
-    constexpr int kLanes = D / 4;                            // of a part
-    constexpr int kAt = kPdJoinThreads / kLanes;             // parts at once
+    using C = PdJoinCfg<D, kAt>;
+    constexpr int kLanes = C::kLanes;
     constexpr int kMost = 4;                                 // kept in registers a lane
-    __shared__ float4 s_acc[kPdJoinThreads];
+    __shared__ float4 s_acc[C::kThreads];
     __shared__ float s_m[kAt], s_w[kAt];
-    const int64_t row = blockIdx.x;
+    const int64_t row = (int64_t)blockIdx.x * C::kRows + (kAt == 1 ? (int)threadIdx.x / kLanes : 0);
+    if (row >= (int64_t)p.B * p.H) return;
     const int b = (int)(row / p.H), h = (int)(row - (int64_t)b * p.H);
     const int hkv = h / p.G, g = h - hkv * p.G, hb = g / heads;
     const int2 sp = p.split[((int64_t)b * p.H_kv + hkv) * p.hblk + hb];
@@ -787,7 +814,7 @@ __global__ void __launch_bounds__(kPdJoinThreads)
                                     : blk1 * 2 * warps + w1;
         return slot * heads + hh;
     };
-    const int mine = (int)threadIdx.x / kLanes, c = (int)threadIdx.x % kLanes;
+    const int mine = kAt == 1 ? 0 : (int)threadIdx.x / kLanes, c = (int)threadIdx.x % kLanes;
     float m = -INFINITY, wsum = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int i0 = mine; i0 < parts; i0 += kAt * kMost) {
@@ -825,28 +852,31 @@ __global__ void __launch_bounds__(kPdJoinThreads)
             acc.w = fmaf(w, v[u].w, acc.w);
         }
     }
-    s_acc[threadIdx.x] = acc;
-    if (c == 0) {
-        s_m[mine] = m;
-        s_w[mine] = wsum;
-    }
-    __syncthreads();
-    if (mine != 0) return;
-    float mx = -INFINITY;
+    float ref = m == -INFINITY ? 0.f : m, sum = wsum;
+    float4 t = acc;
+    if constexpr (kAt > 1) {
+        s_acc[threadIdx.x] = acc;
+        if (c == 0) {
+            s_m[mine] = m;
+            s_w[mine] = wsum;
+        }
+        __syncthreads();
+        if (mine != 0) return;
 #pragma unroll
-    for (int k = 0; k < kAt; ++k) mx = fmaxf(mx, s_m[k]);
-    const float ref = mx == -INFINITY ? 0.f : mx;
-    float4 t = make_float4(0.f, 0.f, 0.f, 0.f);
-    float sum = 0.f;
+        for (int k = 0; k < kAt; ++k) m = fmaxf(m, s_m[k]);
+        ref = m == -INFINITY ? 0.f : m;
+        t = make_float4(0.f, 0.f, 0.f, 0.f);
+        sum = 0.f;
 #pragma unroll
-    for (int k = 0; k < kAt; ++k) {
-        const float w = s_m[k] == -INFINITY ? 1.f : exp2f(s_m[k] - ref);   // 1: of 0, or NaN
-        const float4 a = s_acc[k * kLanes + c];
-        sum = fmaf(w, s_w[k], sum);
-        t.x = fmaf(w, a.x, t.x);
-        t.y = fmaf(w, a.y, t.y);
-        t.z = fmaf(w, a.z, t.z);
-        t.w = fmaf(w, a.w, t.w);
+        for (int k = 0; k < kAt; ++k) {
+            const float w = s_m[k] == -INFINITY ? 1.f : exp2f(s_m[k] - ref);   // 1: of 0, or NaN
+            const float4 a = s_acc[k * kLanes + c];
+            sum = fmaf(w, s_w[k], sum);
+            t.x = fmaf(w, a.x, t.x);
+            t.y = fmaf(w, a.y, t.y);
+            t.z = fmaf(w, a.z, t.z);
+            t.w = fmaf(w, a.w, t.w);
+        }
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
     *reinterpret_cast<uint2*>(p.o + row * D + c * 4) =
