@@ -56,6 +56,7 @@
 namespace fa {
 
 constexpr int kPdBlocks = 148;             // one block an SM
+constexpr int kPdWarpsMost = 12;           // warps of a block, at most
 
 template <int D, int E, int NT>
 struct PdCfg {
@@ -63,19 +64,19 @@ struct PdCfg {
     static constexpr int kStep = kRow <= 128 ? 32 : 16;                   // keys of a step
     static constexpr int kGroups = kStep / 16;
     static constexpr int kStage = 2 * kStep * kRow;                       // K and V of a step
-    static constexpr int kWarps = kRow >= 512 ? 4 : 8;
+    static constexpr int kWarps = kRow >= 512 ? 6 : (D == 128 && E == 1 && NT == 1) ? 12 : 8;
     static constexpr int kThreads = 32 * kWarps;
-    static constexpr int kStages = kRow >= 128 ? 3 : 6;
+    static constexpr int kStages = kWarps == 12 || kWarps == 6 ? 2 : kRow >= 128 ? 3 : 6;
     static constexpr int kHeads = 8 * NT;
     static constexpr int kPitch = D + 4;                                  // of the merge buffer
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kMerge = kWarps * kHeads * kPitch * 4;           // in the ring's place
     static constexpr int kStat = 3 * kWarps * kHeads * 4;                 // m, l, lr
     static constexpr int kSmem = kRing + kStat + kWarps * kStages * 4;
+    static_assert(kWarps <= kPdWarpsMost, "parts of a block");
     static_assert(kMerge <= kRing, "the merge buffer reuses the ring");
     static_assert(kSmem <= 226 * 1024, "shared memory per block");
 };
-constexpr int kPdWarpsMost = 8;
 
 struct PdParams {
     const __nv_bfloat16* q;
@@ -186,21 +187,30 @@ __device__ __forceinline__ int seq_len(const PdParams& p, int b) {
     return (int)max((int64_t)0, min((int64_t)p.kv_len[b], most));
 }
 
-// A place in the line of steps.
+// A place in the line of steps: all sequences for the first unit index (K/V
+// head and block of query heads), then all for the next. Keys of the same
+// tokens are then read for all heads at about the same time, which matters
+// where a token's heads lie side by side (@ORDER@). The next sequence's length
+// is fetched one sequence ahead.
 struct PdCursor {
-    int b, unit, step, n, len;
+    int b, unit, step, n, len, next_len;
 };
 
+__device__ __forceinline__ int pd_peek(const PdParams& p, int b) {
+    return seq_len(p, b + 1 < p.B ? b + 1 : 0);
+}
+
 template <int kStep>
-__device__ __forceinline__ void pd_next(const PdParams& p, PdCursor& c, int units) {
+__device__ __forceinline__ void pd_next(const PdParams& p, PdCursor& c) {
     if (++c.step < c.n) return;
     c.step = 0;
-    if (++c.unit < units) return;
-    c.unit = 0;
-    if (++c.b < p.B) {
-        c.len = seq_len(p, c.b);
-        c.n = steps_of<kStep>(c.len);
+    if (++c.b == p.B) {
+        c.b = 0;
+        ++c.unit;
     }
+    c.len = c.next_len;
+    c.n = steps_of<kStep>(c.len);
+    c.next_len = pd_peek(p, c.b);
 }
 
 template <int D, int E, int NT>
@@ -234,7 +244,7 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
         const int64_t up = __shfl_up_sync(0xffffffffu, incl, off);
         if (lane >= off) incl += up;
     }
-    const int64_t all = __shfl_sync(0xffffffffu, incl, 31) * units;
+    const int64_t total = __shfl_sync(0xffffffffu, incl, 31), all = total * units;
     // With fewer steps than warps, the first `busy` warps take one step each,
     // spread over the blocks: a unit's parts then lie in consecutive workers,
     // none of them without work.
@@ -248,7 +258,8 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
     const int64_t t_lo = worker * quota + min((int64_t)worker, extra);
     PdCursor cur{};
     if (works) {                                             // uniform in the warp
-        const int64_t want = div_pos(t_lo, units);           // in steps of one unit a sequence
+        cur.unit = (int)div_pos(t_lo, total);
+        const int64_t want = t_lo - cur.unit * total;        // in steps of one unit a sequence
         int64_t at = incl - mine;
         const bool owner = at <= want && want < incl;        // one lane
         int b = b_lo, n = 1;
@@ -265,9 +276,8 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
         cur.b = __shfl_sync(0xffffffffu, b, who);
         cur.len = __shfl_sync(0xffffffffu, b_len, who);
         cur.n = __shfl_sync(0xffffffffu, n, who);
-        const int64_t in_seq = t_lo - __shfl_sync(0xffffffffu, at, who) * units;
-        cur.unit = (int)div_pos(in_seq, cur.n);
-        cur.step = (int)(in_seq - (int64_t)cur.unit * cur.n);
+        cur.step = (int)(want - __shfl_sync(0xffffffffu, at, who));
+        cur.next_len = pd_peek(p, cur.b);
     }
 
     // ---------------------------------------------------------- loading
@@ -343,7 +353,7 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
             if (lane == 0) my_seen[slot] = mask;
             ++put_i;
             const int was = put.unit;
-            pd_next<C::kStep>(p, put, units);
+            pd_next<C::kStep>(p, put);
             if (put.unit != was) put_head = (put.unit / p.hblk) * p.c_sh;
             lookup();
         }
@@ -497,7 +507,7 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
                     const float alpha = mn == -INFINITY ? 1.f : fast_exp2(m[nt][j] - mn);
                     m[nt][j] = mn;
                     l[nt][j] *= alpha;
-                    lr[nt][j] *= alpha;
+                    if (E == 1) lr[nt][j] *= alpha;
 #pragma unroll
                     for (int mt = 0; mt < D / 16; ++mt) {
                         o[mt][nt][j] *= alpha;
@@ -505,7 +515,7 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
                     }
                 }
         }
-        uint32_t pb[C::kGroups][NT][2];
+        uint32_t pb[C::kGroups][NT][2], pl[C::kGroups][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
@@ -520,8 +530,9 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
                 uint32_t u;
                 if constexpr (E == 2) {
                     u = pack_bf16x2(p0, p1);
-                    lr[nt][0] = add_bf16_lo(u, lr[nt][0]);
-                    lr[nt][1] = add_bf16_hi(u, lr[nt][1]);
+                    pl[g][nt][h] = transpose8x8(
+                        pack_bf16x2(p0 - __uint_as_float(u << 16),
+                                    p1 - __uint_as_float(u & 0xffff0000u)));
                 } else {
                     u = pack_f16x2(p0, p1);
                     const float2 f = __half22float2(*reinterpret_cast<__half2*>(&u));
@@ -539,8 +550,10 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
                     uint32_t a[4];
                     ldsm4_t(vb + stage_at<C::kRow>(g * 16 + (vg >> 1) * 8 + vi, 2 * mt + (vg & 1)), a);
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                    for (int nt = 0; nt < NT; ++nt) {
                         mma16816<E>(o[mt][nt], a, pb[g][nt][0], pb[g][nt][1]);
+                        mma16816<E>(o[mt][nt], a, pl[g][nt][0], pl[g][nt][1]);
+                    }
                 }
             } else {
                 // a transposed 16-bit block gives, for head-dim pair 2 qr, 2 qr + 1
@@ -573,7 +586,8 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) {
                     l[nt][j] += __shfl_xor_sync(0xffffffffu, l[nt][j], off);
-                    lr[nt][j] += __shfl_xor_sync(0xffffffffu, lr[nt][j], off);
+                    if (E == 1) lr[nt][j] += __shfl_xor_sync(0xffffffffu, lr[nt][j], off);
+                    else lr[nt][j] = l[nt][j];
                 }
     };
     // log2-sum-exp of exact sum `sum` with reference m: -inf for no key at all
@@ -681,7 +695,7 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
             if (grouped) break;
         }
         if (more) {
-            pd_next<C::kStep>(p, cur, units);
+            pd_next<C::kStep>(p, cur);
             load_q();
         }
         finish(b, unit, ends && from_start, ends ? 0 : 1);
