@@ -65,22 +65,23 @@ bool meets_cache(const fa_paged_cache_t& c, size_t bytes, const void* p, size_t 
 
 // ------------------------------------------------------------------ append
 template <int D, bool kNorm, bool kInter>
-void launch_append_d(RotParams p, int elem, cudaStream_t s) {
-    const int64_t blocks = rot_tiling(&p, RotCfg<D>::kSlots, p.H + 2 * p.H_kv);
+void launch_append_d(const RotParams& p, unsigned blocks, int elem, cudaStream_t s) {
     if (elem == 1)
-        fa_qk_rotary_fwd<D, kNorm, kInter, kPageE4m3><<<(unsigned)blocks, kRotThreads, 0, s>>>(p);
+        fa_qk_rotary_fwd<D, kNorm, kInter, kPageE4m3><<<blocks, kRotThreads, 0, s>>>(p);
     else
-        fa_qk_rotary_fwd<D, kNorm, kInter, kPageBf16><<<(unsigned)blocks, kRotThreads, 0, s>>>(p);
+        fa_qk_rotary_fwd<D, kNorm, kInter, kPageBf16><<<blocks, kRotThreads, 0, s>>>(p);
 }
 
 template <int D>
-void launch_append(const RotParams& p, int elem, bool norm, bool inter, cudaStream_t s) {
+int launch_append(RotParams p, int elem, bool norm, bool inter, cudaStream_t s) {
+    const unsigned n = rot_grid(&p, RotCfg<D>::kSlots, p.H + 2 * p.H_kv);
     if (norm)
-        inter ? launch_append_d<D, true, true>(p, elem, s)
-              : launch_append_d<D, true, false>(p, elem, s);
+        inter ? launch_append_d<D, true, true>(p, n, elem, s)
+              : launch_append_d<D, true, false>(p, n, elem, s);
     else
-        inter ? launch_append_d<D, false, true>(p, elem, s)
-              : launch_append_d<D, false, false>(p, elem, s);
+        inter ? launch_append_d<D, false, true>(p, n, elem, s)
+              : launch_append_d<D, false, false>(p, n, elem, s);
+    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
 int append(const fa_paged_append_t& a, void* stream) {
@@ -90,7 +91,8 @@ int append(const fa_paged_append_t& a, void* stream) {
     if (rc == FA_OK) rc = rotary_check(a.rotary, c.d);
     if (rc == FA_OK) rc = table_check(a.table);
     if (rc != FA_OK) return rc;
-    if (a.B < 0 || a.H < 0 || a.N < 0 || (int64_t)a.B * a.N > INT32_MAX || a.H > 65536)
+    if (a.B < 0 || a.H < 0 || a.N < 0 || (int64_t)a.B * a.N > INT32_MAX || a.H > 65536 ||
+        (double)a.B * a.N * ((double)a.H + 2.0 * c.H_kv) > INT32_MAX)   // rows in 31 bits
         return FA_ERR_INVALID_ARG;
     if ((a.q.ptr == nullptr) != (a.q_out.ptr == nullptr)) return FA_ERR_INVALID_ARG;
     const int H = a.q.ptr == nullptr ? 0 : a.H;
@@ -135,10 +137,9 @@ int append(const fa_paged_append_t& a, void* stream) {
     p.v_inv = 1.f / c.v_descale;
     const bool norm = a.rotary.norm != 0, inter = a.rotary.interleaved != 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (c.d == 64) launch_append<64>(p, c.elem, norm, inter, s);
-    else if (c.d == 128) launch_append<128>(p, c.elem, norm, inter, s);
-    else launch_append<256>(p, c.elem, norm, inter, s);
-    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+    return c.d == 64    ? launch_append<64>(p, c.elem, norm, inter, s)
+           : c.d == 128 ? launch_append<128>(p, c.elem, norm, inter, s)
+                        : launch_append<256>(p, c.elem, norm, inter, s);
 }
 
 // ------------------------------------------------------------------ decode

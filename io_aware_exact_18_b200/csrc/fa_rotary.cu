@@ -28,7 +28,10 @@ namespace {
 // the grid 31.
 int sizes_check(int B, int H, int H_kv, int N) {
     if (B < 0 || H < 0 || H_kv < 0 || N < 0) return FA_ERR_INVALID_ARG;
-    if ((int64_t)B * N > INT32_MAX || H > 65536 || H_kv > 65536) return FA_ERR_INVALID_ARG;
+    if (H > 65536 || H_kv > 65536) return FA_ERR_INVALID_ARG;
+    // rows (and so units of work) are counted in 31 bits
+    if ((double)B * N * ((double)H + H_kv) > INT32_MAX) return FA_ERR_INVALID_ARG;
+    if ((int64_t)B * N > INT32_MAX) return FA_ERR_INVALID_ARG;
     return FA_OK;
 }
 
@@ -51,22 +54,22 @@ int views_check(const View* in, int n_in, const View* out, int n_out, const int*
 }
 
 template <int D, bool kNorm, bool kInter>
-void launch_fwd_d(RotParams p, cudaStream_t s) {
-    const int64_t blocks = rot_tiling(&p, RotCfg<D>::kSlots, p.H + p.H_kv);
-    fa_qk_rotary_fwd<D, kNorm, kInter, kDense><<<(unsigned)blocks, kRotThreads, 0, s>>>(p);
+void launch_fwd_d(RotParams p, unsigned blocks, cudaStream_t s) {
+    fa_qk_rotary_fwd<D, kNorm, kInter, kDense><<<blocks, kRotThreads, 0, s>>>(p);
 }
 
 template <int D>
-void launch_fwd(const RotParams& p, bool norm, bool inter, cudaStream_t s) {
-    if (norm) inter ? launch_fwd_d<D, true, true>(p, s) : launch_fwd_d<D, true, false>(p, s);
-    else inter ? launch_fwd_d<D, false, true>(p, s) : launch_fwd_d<D, false, false>(p, s);
+int launch_fwd(RotParams p, bool norm, bool inter, cudaStream_t s) {
+    const unsigned n = rot_grid(&p, RotCfg<D>::kSlots, p.H + p.H_kv);
+    if (norm) inter ? launch_fwd_d<D, true, true>(p, n, s) : launch_fwd_d<D, true, false>(p, n, s);
+    else inter ? launch_fwd_d<D, false, true>(p, n, s) : launch_fwd_d<D, false, false>(p, n, s);
+    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
 int launch_fwd_any(const RotParams& p, int d, bool norm, bool inter, cudaStream_t s) {
-    if (d == 64) launch_fwd<64>(p, norm, inter, s);
-    else if (d == 128) launch_fwd<128>(p, norm, inter, s);
-    else launch_fwd<256>(p, norm, inter, s);
-    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+    return d == 64    ? launch_fwd<64>(p, norm, inter, s)
+           : d == 128 ? launch_fwd<128>(p, norm, inter, s)
+                      : launch_fwd<256>(p, norm, inter, s);
 }
 
 int fwd(const fa_qk_rotary_t& a, void* stream) {
@@ -98,23 +101,40 @@ int fwd(const fa_qk_rotary_t& a, void* stream) {
 int slots_of(int d) { return d == 64 ? RotCfg<64>::kSlots : d == 128 ? RotCfg<128>::kSlots
                                                                      : RotCfg<256>::kSlots; }
 
-// Blocks of the backward with the norm: its items, up to kRotBwdBlocks.
-int64_t bwd_blocks(int B, int H, int H_kv, int N, int d, int64_t* items) {
-    RotParams p{};
-    p.tokens = (int64_t)B * N;
-    *items = rot_tiling(&p, slots_of(d), H + H_kv);
-    return std::min<int64_t>(*items, kRotBwdBlocks);
+// Steps and blocks of the backward with the norm, q's and k's blocks in
+// proportion to their heads.
+int bwd_blocks(RotBwdParams* bp, int slots) {
+    const int64_t tiles = rot_tiles(&bp->f, slots);
+    const int H = bp->side[0].heads, H_kv = bp->side[1].heads;
+    int64_t n[2] = {0, 0};
+    for (int i = 0; i < 2; ++i) {
+        RotBwdSide& sd = bp->side[i];
+        if (sd.heads == 0) continue;
+        sd.per_tile = (uint32_t)rot_steps(bp->f, slots, sd.heads);
+        sd.steps = tiles * sd.per_tile;
+        const int64_t share = (int64_t)kRotBwdBlocks * sd.heads / (H + H_kv);
+        n[i] = std::max<int64_t>(1, std::min<int64_t>(sd.steps, share));
+    }
+    bp->q_blocks = (int)n[0];
+    return (int)(n[0] + n[1]);
+}
+
+int bwd_blocks_of(int B, int H, int H_kv, int N, int d) {
+    RotBwdParams bp{};
+    bp.f.tokens = (int64_t)B * N;
+    bp.side[0].heads = H;
+    bp.side[1].heads = H_kv;
+    return bwd_blocks(&bp, slots_of(d));
 }
 
 template <int D>
 int launch_bwd(RotBwdParams bp, bool inter, float* dwq, float* dwk, cudaStream_t s) {
-    bp.items = rot_tiling(&bp.f, RotCfg<D>::kSlots, bp.f.H + bp.f.H_kv);
-    const int blocks = (int)std::min<int64_t>(bp.items, kRotBwdBlocks);
+    const int blocks = bwd_blocks(&bp, RotCfg<D>::kSlots);
     if (inter) fa_qk_rotary_bwd_norm<D, true><<<blocks, kRotThreads, 0, s>>>(bp);
     else fa_qk_rotary_bwd_norm<D, false><<<blocks, kRotThreads, 0, s>>>(bp);
     if (cudaGetLastError() != cudaSuccess) return FA_ERR_LAUNCH;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(2 * D / 32);
+    cfg.gridDim = dim3(D / 32, 2);
     cfg.blockDim = dim3(32, 32);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -122,8 +142,8 @@ int launch_bwd(RotBwdParams bp, bool inter, float* dwq, float* dwk, cudaStream_t
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e =
-        cudaLaunchKernelEx(&cfg, fa_rotary_dw<D>, (const float*)bp.part, blocks, dwq, dwk);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, fa_rotary_dw<D>, (const float*)bp.part, blocks,
+                                             bp.q_blocks, dwq, dwk);
     return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
 }
 
@@ -158,9 +178,8 @@ int bwd(const fa_qk_rotary_bwd_t& a, void* ws, size_t ws_bytes, void* stream) {
     const int replaces[2] = {0, 1};
     rc = views_check(in, norm ? 4 : 2, out, 2, replaces);
     if (rc != FA_OK) return rc;
-    int64_t items = 0;
     const size_t need =
-        norm ? (size_t)bwd_blocks(a.B, a.H, a.H_kv, a.N, a.d, &items) * 2 * a.d * 4 : 0;
+        norm ? (size_t)bwd_blocks_of(a.B, a.H, a.H_kv, a.N, a.d) * a.d * 4 : 0;
     if (norm) {
         if (ws == nullptr || (addr(ws) & 15u) != 0 || ws_bytes < need) return FA_ERR_INVALID_ARG;
         struct Buf { const void* p; size_t n; };
@@ -185,12 +204,10 @@ int bwd(const fa_qk_rotary_bwd_t& a, void* ws, size_t ws_bytes, void* stream) {
         p.k = rot_rows(a.dk_out);
         return launch_fwd_any(p, a.d, false, a.rotary.interleaved, s);
     }
-    p.q = rot_rows(a.q);
-    p.k = rot_rows(a.k);
     RotBwdParams bp{};
     bp.f = p;
-    bp.dq_out = rot_rows(a.dq_out);
-    bp.dk_out = rot_rows(a.dk_out);
+    bp.side[0] = RotBwdSide{rot_rows(a.dq_out), rot_rows(a.q), p.qo, p.wq, a.H, 0, 0};
+    bp.side[1] = RotBwdSide{rot_rows(a.dk_out), rot_rows(a.k), p.ko, p.wk, a.H_kv, 0, 0};
     bp.part = static_cast<float*>(ws);
     const bool inter = a.rotary.interleaved != 0;
     if (a.d == 64) return launch_bwd<64>(bp, inter, a.dq_weight, a.dk_weight, s);
@@ -219,8 +236,7 @@ FA_EXPORT size_t fa_qk_rotary_bwd_workspace_bytes(int B, int H, int H_kv, int N,
     if ((d != 64 && d != 128 && d != 256) || fa::sizes_check(B, H, H_kv, N) != FA_OK || !norm ||
         B == 0 || N == 0 || H + H_kv == 0)
         return 0;
-    int64_t items = 0;
-    return (size_t)fa::bwd_blocks(B, H, H_kv, N, d, &items) * 2 * (size_t)d * 4;
+    return (size_t)fa::bwd_blocks_of(B, H, H_kv, N, d) * (size_t)d * 4;
 }
 
 }  // extern "C"

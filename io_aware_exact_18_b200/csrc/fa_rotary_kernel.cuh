@@ -11,18 +11,23 @@
 // alone, not on the head.
 //
 // What bounds it: HBM, 2 bytes read and 2 written an element (backward with
-// the norm: 4 and 2). So a thread owns one 16-byte chunk (8 elements) of the
-// rows of ONE token, keeps A and B (16 registers) for that token and walks
-// over the heads, four loads in flight. A half-layout chunk's partner is the
-// chunk r/16 lanes away (rotary_dim is a multiple of 16), fetched by shuffle;
-// interleaved partners sit in the chunk itself. A row's d / 8 lanes lie in
-// one warp, so the sum of squares is a shuffle reduction.
+// the norm: 4 and 2), and next to it the instructions: some 45 a 16-byte chunk
+// have to fit into the time that its 32 bytes take. So a thread owns two
+// chunks (8 elements each) of the rows of ONE token, keeps their A and B in
+// registers and walks over the heads. In the half layout they are the two
+// chunks whose elements pair up (rotary_dim is a multiple of 16, so whole
+// chunks do), or two neighbours among those that are not turned; interleaved,
+// neighbours. No element crosses lanes then, and fp32 is multiplied in pairs.
+// (With one chunk a thread, the partner's coming by shuffle, unpacked again:
+// 124 instructions a chunk and 62 us where this takes @FWD@, B1 H32 H_kv8
+// N16384 d128 with the norm.) A row's d / 16 lanes lie in one warp, so the sum
+// of squares is a shuffle reduction.
 //
 // Angles: p f_i is formed in fp64 in turns (f_i / 2 pi), reduced to
 // [-1/2, 1/2] there and only then rounded to fp32 (an error of at most 2^-25
 // turns, 2e-7 rad, at any position); fp32 products would be off by 0.01 rad
 // at position 10^5. A block's angles are computed once, cooperatively, into
-// shared memory: one sincospi a thread for every 10 or so chunks.
+// shared memory: a few sincospi a thread for all its heads.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -32,8 +37,10 @@
 
 namespace fa {
 
-constexpr int kRotThreads = 256;
-constexpr int kRotUnroll = 4;        // heads whose loads a thread keeps in flight
+constexpr int kRotThreads = 128;
+constexpr int kRotUnroll = 4;        // rows of a batch
+constexpr int kRotBlocksPerSm = 4;
+constexpr int kRotFill = 2 * 148;    // blocks of a launch, if the heads of a tile can be split
 
 struct RotRows {                     // one [B, heads, N, d] view, strides in elements
     uint8_t* ptr;
@@ -51,8 +58,9 @@ struct RotParams {
     float cs_scale, sin_sign, eps;
     int B, H, H_kv, N;
     int64_t tokens;                  // B * N
-    int tt_shift;                    // log2 of the tokens of a block
-    int splits;                      // blocks that share a token tile's heads
+    int tt_shift;                    // log2 of the tokens of a tile
+    int pair_shift;                  // log2 of rot / 2, rounded up
+    int splits;                      // blocks that share a tile's heads (forward)
     // append
     uint8_t *kc, *vc;
     int64_t c_sp, c_sh, c_st;        // page, head, token strides in elements
@@ -65,125 +73,184 @@ struct RotParams {
 
 template <int D>
 struct RotCfg {
-    static constexpr int kLanes = D / 8;                     // lanes of a row
+    static constexpr int kLanes = D / 16;                    // lanes of a row, two chunks each
     static constexpr int kSlots = kRotThreads / kLanes;      // rows a block holds at once
     static constexpr int kTable = kSlots * D / 2;            // (cos, sin) of kSlots tokens
 };
 
-__device__ __forceinline__ float bf_lo(uint32_t v) { return __uint_as_float(v << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t v) { return __uint_as_float(v & 0xffff0000u); }
-
-__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
-    x[0] = bf_lo(u.x); x[1] = bf_hi(u.x);
-    x[2] = bf_lo(u.y); x[3] = bf_hi(u.y);
-    x[4] = bf_lo(u.z); x[5] = bf_hi(u.z);
-    x[6] = bf_lo(u.w); x[7] = bf_hi(u.w);
+// Pairs of fp32 in one 64-bit register: sm_100 multiplies and adds them two at
+// a time (each half rounded like the scalar instruction).
+using f2 = uint64_t;
+__device__ __forceinline__ f2 f2_make(float lo, float hi) {
+    f2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ float2 f2_get(f2 v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ f2 f2_mul(f2 a, f2 b) {
+    f2 r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ f2 f2_fma(f2 a, f2 b, f2 c) {
+    f2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ float f2_sum(f2 v) {
+    const float2 t = f2_get(v);
+    return t.x + t.y;
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-    return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                      pack_bf16x2(x[6], x[7]));
+__device__ __forceinline__ f2 bf2(uint32_t v) {          // a bf16 pair, widened
+    return f2_make(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+__device__ __forceinline__ void unpack8(const uint4& u, f2 (&x)[4]) {
+    x[0] = bf2(u.x);
+    x[1] = bf2(u.y);
+    x[2] = bf2(u.z);
+    x[3] = bf2(u.w);
+}
+__device__ __forceinline__ uint32_t pack2(f2 v) {
+    const float2 t = f2_get(v);
+    return pack_bf16x2(t.x, t.y);
+}
+__device__ __forceinline__ uint4 pack8(const f2 (&x)[4]) {
+    return make_uint4(pack2(x[0]), pack2(x[1]), pack2(x[2]), pack2(x[3]));
 }
 
-__device__ __forceinline__ float norm_weight(const void* w, int w32, int i) {
-    if (w == nullptr) return 1.f;
-    return w32 ? static_cast<const float*>(w)[i]
-               : __bfloat162float(static_cast<const __nv_bfloat16*>(w)[i]);
-}
-
-// (s cos, s sin) of the block's tokens into shared memory. With `pad`, tokens
-// outside the batch or at negative positions give position 0 (never used).
-__device__ __forceinline__ void rotary_table(float2* cs, const RotParams& p, int64_t tok0, int tt,
-                                             int tid) {
-    const int half = p.rot >> 1;
-    for (int e = tid; e < tt * half; e += kRotThreads) {
-        const int t = e / half, i = e - t * half;
-        const int64_t tok = tok0 + t;
-        float c = 0.f, s = 0.f;
-        if (tok < p.tokens) {
-            const int64_t b = tok / p.N, n = tok - b * p.N;
-            const int32_t pos = p.pos[b * p.pos_sb + n * p.pos_sn];
-            double turns = (double)pos * p.freqs[i] * 0.15915494309189533577;
-            turns -= rint(turns);
-            sincospif(2.f * (float)turns, &s, &c);
+// Norm weights of the 8 elements of chunk c.
+__device__ __forceinline__ void norm_weights(const void* w, int w32, int c, f2 (&x)[4]) {
+    if (w == nullptr) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[j] = f2_make(1.f, 1.f);
+    } else if (w32) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float* src = static_cast<const float*>(w) + c * 8 + 2 * j;
+            x[j] = f2_make(src[0], src[1]);
         }
-        cs[e] = make_float2(c * p.cs_scale, s * p.cs_scale * p.sin_sign);
+    } else {
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(w) + c * 8;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            x[j] = f2_make(__bfloat162float(src[2 * j]), __bfloat162float(src[2 * j + 1]));
     }
 }
 
-// Where a chunk stands in the rotation: whether it is turned, the lane of its
-// partner chunk (half layout) and its first pair.
-struct ChunkRole {
-    bool turned, second;
-    int partner, pair0;
+// Token `tok` of the batch, as (b, n). Tokens number less than 2^31.
+struct RotToken {
+    int64_t b, n;
+};
+__device__ __forceinline__ RotToken rot_token(const RotParams& p, int64_t tok) {
+    const uint32_t b = (uint32_t)tok / (uint32_t)p.N;
+    return RotToken{(int64_t)b, tok - (int64_t)b * p.N};
+}
+
+// (s cos, s sin) of the block's tokens into shared memory (unused past the
+// last token). A thread stays with one pair; (b0, n0) is the first token.
+__device__ __forceinline__ void rotary_table(float2* cs, const RotParams& p, int64_t tok0,
+                                             const RotToken& t0, int tt, int tid) {
+    const int half = p.rot >> 1, i = tid & ((1 << p.pair_shift) - 1);
+    if (i >= half) return;
+    const double turn = p.freqs[i] * 0.15915494309189533577;
+    for (int t = tid >> p.pair_shift; t < tt; t += kRotThreads >> p.pair_shift) {
+        if (tok0 + t >= p.tokens) break;
+        RotToken at{t0.b, t0.n + t};
+        if (at.n >= p.N) at = rot_token(p, tok0 + t);
+        double turns = (double)p.pos[at.b * p.pos_sb + at.n * p.pos_sn] * turn;
+        turns -= rint(turns);
+        float c, s;
+        sincospif(2.f * (float)turns, &s, &c);
+        cs[t * half + i] = make_float2(c * p.cs_scale, s * p.cs_scale * p.sin_sign);
+    }
+}
+
+// A lane's two chunks and their place in the rotation: whether they are
+// turned, and their first pair of eight.
+struct LaneRole {
+    int c0, c1;
+    bool turned;
+    int pair0;
 };
 
-template <int D, bool kInter>
-__device__ __forceinline__ ChunkRole chunk_role(int c, int lane, int rot) {
-    ChunkRole r;
-    const int e0 = c * 8, half = rot >> 1;
-    r.turned = e0 < rot;
-    r.partner = lane;
-    if constexpr (kInter) {
-        r.second = false;
-        r.pair0 = e0 >> 1;
+template <bool kInter>
+__device__ __forceinline__ LaneRole lane_role(int l, int rot) {
+    LaneRole r;
+    const int both = rot >> 4;                               // lanes whose chunks are turned
+    r.turned = l < both;
+    r.pair0 = 8 * l;
+    if (kInter || !r.turned) {                               // the half layout's turned lanes
+        r.c0 = 2 * l;                                        // use up chunks [0, 2 both) too
+        r.c1 = 2 * l + 1;
     } else {
-        r.second = r.turned && e0 >= half;
-        r.pair0 = r.second ? e0 - half : e0;
-        if (r.turned) r.partner = r.second ? lane - (half >> 3) : lane + (half >> 3);
+        r.c0 = l;
+        r.c1 = l + both;
     }
     return r;
 }
 
-// cos and signed sin of a chunk's elements: out_e = c_e y_e + s_e y_partner.
+// Coefficients of the turned pairs: y0 = a0 x0 + b0 p0 and y1 = a1 x1 + b1 p1
+// for a lane's chunks x0, x1 and their partners' elements p0, p1.
+struct LaneAngles {
+    f2 a0[4], b0[4], a1[4], b1[4];
+};
+
 template <bool kInter>
-__device__ __forceinline__ void chunk_angles(const float2* cs, const ChunkRole& r, float (&co)[8],
-                                             float (&si)[8]) {
+__device__ __forceinline__ void lane_angles(const float2* cs, const LaneRole& r, LaneAngles& t) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        co[e] = 1.f;
-        si[e] = 0.f;
+    for (int j = 0; j < 4; ++j) {
+        t.a0[j] = t.a1[j] = f2_make(1.f, 1.f);
+        t.b0[j] = t.b1[j] = f2_make(0.f, 0.f);
     }
     if (!r.turned) return;
-    if constexpr (kInter) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 t = cs[r.pair0 + j];
-            co[2 * j] = co[2 * j + 1] = t.x;
-            si[2 * j] = -t.y;
-            si[2 * j + 1] = t.y;
-        }
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float2 t = cs[r.pair0 + e];
-            co[e] = t.x;
-            si[e] = r.second ? t.y : -t.y;
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (kInter) {                              // one pair in two elements
+            const float2 u = cs[r.pair0 + j], v = cs[r.pair0 + 4 + j];
+            t.a0[j] = f2_make(u.x, u.x);
+            t.b0[j] = f2_make(-u.y, u.y);
+            t.a1[j] = f2_make(v.x, v.x);
+            t.b1[j] = f2_make(-v.y, v.y);
+        } else {                                             // two pairs, half of each
+            const float4 u = *reinterpret_cast<const float4*>(cs + r.pair0 + 2 * j);
+            t.a0[j] = t.a1[j] = f2_make(u.x, u.z);
+            t.b0[j] = f2_make(-u.y, -u.w);
+            t.b1[j] = f2_make(u.y, u.w);
         }
     }
 }
 
-// The partners of a chunk's 8 elements. Elements that are not turned get 0,
-// so that an infinity there is not multiplied by a zero coefficient.
+// a x + b p for a lane's chunk x and its partners' elements p. In interleaved
+// pairs p is x with its halves swapped, which costs as many moves as the
+// products in pairs save: there they are taken one by one.
 template <bool kInter>
-__device__ __forceinline__ void chunk_partners(const uint4& u, const ChunkRole& r,
-                                               float (&xp)[8]) {
-    if constexpr (kInter) {
-        float x[8];
-        unpack8(u, x);
+__device__ __forceinline__ f2 turn2(f2 a, f2 x, f2 b, f2 p) {
+    if constexpr (!kInter) return f2_fma(a, x, f2_mul(b, p));
+    const float2 ca = f2_get(a), cb = f2_get(b), u = f2_get(x), v = f2_get(p);
+    return f2_make(fmaf(ca.x, u.x, cb.x * v.x), fmaf(ca.y, u.y, cb.y * v.y));
+}
+
+// The partners' elements. Where `part` of the head is turned, lanes that are
+// not get 0, so that an infinity there is not multiplied by a zero coefficient.
+template <bool kInter>
+__device__ __forceinline__ void lane_partners(const f2 (&x0)[4], const f2 (&x1)[4], bool zero,
+                                              f2 (&p0)[4], f2 (&p1)[4]) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            xp[2 * j] = r.turned ? x[2 * j + 1] : 0.f;
-            xp[2 * j + 1] = r.turned ? x[2 * j] : 0.f;
+    for (int j = 0; j < 4; ++j) {
+        if constexpr (kInter) {
+            const float2 u = f2_get(x0[j]), v = f2_get(x1[j]);
+            p0[j] = f2_make(u.y, u.x);
+            p1[j] = f2_make(v.y, v.x);
+        } else {
+            p0[j] = x1[j];
+            p1[j] = x0[j];
         }
-    } else {
-        uint4 o;
-        o.x = __shfl_sync(0xffffffffu, u.x, r.partner);
-        o.y = __shfl_sync(0xffffffffu, u.y, r.partner);
-        o.z = __shfl_sync(0xffffffffu, u.z, r.partner);
-        o.w = __shfl_sync(0xffffffffu, u.w, r.partner);
-        if (!r.turned) o = make_uint4(0u, 0u, 0u, 0u);
-        unpack8(o, xp);
+        if (zero) p0[j] = p1[j] = 0ull;
     }
 }
 
@@ -196,181 +263,202 @@ __device__ __forceinline__ float row_sum(float v) {
 
 enum RotStore { kDense = 0, kPageBf16 = 1, kPageE4m3 = 2 };
 
-// Eight fp32 values to a cache row chunk (8 codes or 8 bf16 at element c * 8).
+// Eight fp32 values to a row chunk (8 codes or 8 bf16 at element c * 8).
 template <bool kE4m3>
-__device__ __forceinline__ void store_chunk(uint8_t* row, int c, const float (&y)[8]) {
-    if constexpr (kE4m3)
-        *reinterpret_cast<uint2*>(row + c * 8) = make_uint2(
-            pack_e4m3x4(y[0], y[1], y[2], y[3]), pack_e4m3x4(y[4], y[5], y[6], y[7]));
-    else
+__device__ __forceinline__ void store_chunk(uint8_t* row, int c, const f2 (&y)[4]) {
+    if constexpr (kE4m3) {
+        const float2 a = f2_get(y[0]), b = f2_get(y[1]), d = f2_get(y[2]), e = f2_get(y[3]);
+        *reinterpret_cast<uint2*>(row + c * 8) =
+            make_uint2(pack_e4m3x4(a.x, a.y, b.x, b.y), pack_e4m3x4(d.x, d.y, e.x, e.y));
+    } else {
         *reinterpret_cast<uint4*>(row + c * 16) = pack8(y);
-}
-
-// Heads [h_lo, h_hi) of one input for this thread's token: load, norm, turn,
-// store. `in` and `out` point at head 0 of the token; strides in bytes. `mul`
-// (1 / descale of an e4m3 store) is part of A and B already.
-template <int D, bool kNorm, bool kInter, bool kE4m3>
-__device__ __forceinline__ void turn_heads(const uint8_t* in, int64_t in_sh, uint8_t* out,
-                                           int64_t out_sh, int h_lo, int h_hi, int h_off,
-                                           int h_step, bool live, bool store, int c,
-                                           const ChunkRole& role, const float (&A)[8],
-                                           const float (&Bc)[8], float eps) {
-    for (int h0 = h_lo; h0 < h_hi; h0 += h_step * kRotUnroll) {
-        uint4 u[kRotUnroll];
-#pragma unroll
-        for (int i = 0; i < kRotUnroll; ++i) {
-            const int h = h0 + i * h_step + h_off;
-            u[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (live && h < h_hi)
-                u[i] = *reinterpret_cast<const uint4*>(in + h * in_sh + c * 16);
-        }
-#pragma unroll
-        for (int i = 0; i < kRotUnroll; ++i) {
-            if (h0 + i * h_step >= h_hi) break;              // uniform in the block
-            const int h = h0 + i * h_step + h_off;
-            float x[8], xp[8], y[8];
-            unpack8(u[i], x);
-            chunk_partners<kInter>(u[i], role, xp);
-            float r = 1.f;
-            if constexpr (kNorm) {
-                float ss = 0.f;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-                ss = row_sum<D / 8>(ss);
-                r = rsqrtf(fmaf(ss, 1.f / D, eps));
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                y[e] = fmaf(A[e], x[e], Bc[e] * xp[e]);
-                if constexpr (kNorm) y[e] *= r;
-            }
-            if (!(store && h < h_hi)) continue;
-            if (!kNorm && !kE4m3 && !role.turned)            // passes through bit for bit
-                *reinterpret_cast<uint4*>(out + h * out_sh + c * 16) = u[i];
-            else
-                store_chunk<kE4m3>(out + h * out_sh, c, y);
-        }
     }
 }
 
-// A and B of one chunk: angles times the norm's weights (the partner's for B).
+// The coefficients times the norm's weights (the partners' for b) and `mul`.
 template <int D, bool kNorm, bool kInter>
-__device__ __forceinline__ void coefficients(const float2* cs, const ChunkRole& role, int c,
-                                             int rot, const void* w, int w32, float mul,
-                                             float (&A)[8], float (&Bc)[8]) {
-    chunk_angles<kInter>(cs, role, A, Bc);
+__device__ __forceinline__ void coefficients(const float2* cs, const LaneRole& role, const void* w,
+                                             int w32, float mul, LaneAngles& t) {
+    lane_angles<kInter>(cs, role, t);
+    const f2 mm = f2_make(mul, mul);
+    f2 w0[4], w1[4], v0[4], v1[4];
+    if constexpr (kNorm) {
+        norm_weights(w, w32, role.c0, w0);
+        norm_weights(w, w32, role.c1, w1);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-        float wa = mul, wb = mul;
-        if constexpr (kNorm) {
-            const int i = c * 8 + e;
-            int j = i;
-            if (role.turned) {
-                if constexpr (kInter) j = i ^ 1;
-                else j = role.second ? i - (rot >> 1) : i + (rot >> 1);
-            }
-            wa *= norm_weight(w, w32, i);
-            wb *= norm_weight(w, w32, j);
+        for (int j = 0; j < 4; ++j) {
+            w0[j] = f2_mul(w0[j], mm);
+            w1[j] = f2_mul(w1[j], mm);
         }
-        A[e] *= wa;
-        Bc[e] *= wb;
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w0[j] = w1[j] = mm;
+    }
+    lane_partners<kInter>(w0, w1, false, v0, v1);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        t.a0[j] = f2_mul(t.a0[j], w0[j]);
+        t.b0[j] = f2_mul(t.b0[j], v0[j]);
+        t.a1[j] = f2_mul(t.a1[j], w1[j]);
+        t.b1[j] = f2_mul(t.b1[j], v1[j]);
     }
 }
 
 // Block (token tile, head split). Virtual heads: the H of q, the H_kv of k
-// and, appending, the H_kv of v; a split takes an even share of them.
+// and, appending, the H_kv of v; a split takes an even share of them, and a
+// thread goes through its own in batches of kRotUnroll rows (two chunks each)
+// kept on the way in registers, the first batch while the angles are computed.
+// What decides the speed is the bytes on the way: batches of two, three and
+// four rows took 75, 67 and 62 us (B1 H32 H_kv8 N16384 d128 with the norm,
+// 51 us at the copy rate). Tried, and no faster: the work shared out evenly
+// over one round of blocks (62 us; 1024 tiles over 592 places are two rounds
+// for the work of 1.7), more splits (65 us with two: each computes the angles
+// again), and rows fetched by cp.async up to eight ahead (63 us; interleaved
+// pairs 85 instead of 60: the bookkeeping of single rows costs more
+// instructions than the loads on the way give back).
 template <int D, bool kNorm, bool kInter, int kStore>
-__global__ void __launch_bounds__(kRotThreads) fa_qk_rotary_fwd(const RotParams p) {
+__global__ void __launch_bounds__(kRotThreads, kRotBlocksPerSm) fa_qk_rotary_fwd(const RotParams p) {
     using C = RotCfg<D>;
     __shared__ __align__(16) float2 cs[C::kTable];
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int tid = threadIdx.x;
     const int tt = 1 << p.tt_shift;
-    const int64_t tile = blockIdx.x / (unsigned)p.splits;
+    const uint32_t tile = blockIdx.x / (uint32_t)p.splits;
     const int split = (int)(blockIdx.x - tile * p.splits);
-    const int64_t tok0 = tile * tt;
+    const int64_t tok0 = (int64_t)tile * tt;
     const int heads = p.H + p.H_kv + (kStore != kDense ? p.H_kv : 0);
     const int lo = (int)((int64_t)heads * split / p.splits);
     const int hi = (int)((int64_t)heads * (split + 1) / p.splits);
-    if (lo < p.H + p.H_kv) rotary_table(cs, p, tok0, tt, tid);
+    const int slot = tid / C::kLanes;
+    const int ts = slot & (tt - 1), h_off = slot >> p.tt_shift, h_step = C::kSlots >> p.tt_shift;
+    const LaneRole role = lane_role<kInter>(tid % C::kLanes, p.rot);
+    const bool pass = !role.turned;                          // some lanes where part is turned
+    const bool part = p.rot < D;
+    const bool live = tok0 + ts < p.tokens;
+    const RotToken t0 = rot_token(p, tok0);
+    RotToken at{t0.b, t0.n + ts};
+    if (at.n >= p.N) at = rot_token(p, live ? tok0 + ts : 0);
+
+    // A batch: heads h0 + i h_step + h_off, i < kRotUnroll, below end, of one
+    // input (0 q, 1 k, 2 v). Past the last head the last is loaded again, and
+    // past the last token the first: those rows are computed and not stored.
+    auto load = [&](int input, int h0, int h_end, uint4 (&u)[kRotUnroll][2]) {
+        const RotRows& r = input == 0 ? p.q : input == 1 ? p.k : p.v;
+        const uint8_t* src = r.ptr + (at.b * r.sb + at.n * r.sn) * 2;
+        const int64_t sh = r.sh * 2;
+#pragma unroll
+        for (int i = 0; i < kRotUnroll; ++i) {
+            const uint8_t* row = src + min(h0 + i * h_step + h_off, h_end - 1) * sh;
+            u[i][0] = *reinterpret_cast<const uint4*>(row + role.c0 * 16);
+            u[i][1] = *reinterpret_cast<const uint4*>(row + role.c1 * 16);
+        }
+    };
+    int input = lo < p.H ? 0 : lo < p.H + p.H_kv ? 1 : 2;
+    int before = input == 0 ? 0 : input == 1 ? p.H : p.H + p.H_kv;        // virtual heads
+    uint4 u[kRotUnroll][2];
+    load(input, lo - before, min(hi - before, input == 0 ? p.H : p.H_kv), u);
+    if (input < 2) rotary_table(cs, p, tok0, t0, tt, tid);
     __syncthreads();
 
-    const int c = tid % C::kLanes, slot = tid / C::kLanes;
-    const int ts = slot & (tt - 1), h_off = slot >> p.tt_shift, h_step = C::kSlots >> p.tt_shift;
-    const int64_t tok = tok0 + ts;
-    const bool live = tok < p.tokens;
-    const int64_t b = live ? tok / p.N : 0, n = live ? tok - b * p.N : 0;
-    const ChunkRole role = chunk_role<D, kInter>(c, lane, p.rot);
-    const float2* my_cs = cs + ts * (p.rot >> 1);
-
     bool write = live, stored = live;
-    uint8_t *kdst = nullptr, *vdst = nullptr;
-    int64_t dst_sh = 0;
+    uint8_t *k_out = nullptr, *v_out = nullptr;
+    int64_t out_sh = 0;
     constexpr int kElem = kStore == kPageE4m3 ? 1 : 2;
     if constexpr (kStore != kDense) {
         // the token's slot in the cache, every index checked
         int32_t pos = -1;
-        if (live) pos = p.pos[b * p.pos_sb + n * p.pos_sn];
+        if (live) pos = p.pos[at.b * p.pos_sb + at.n * p.pos_sn];
         write = pos >= 0;
         stored = false;
         if (write) {
-            const int64_t row = p.seq != nullptr ? p.seq[b] : b;
+            const int64_t row = p.seq != nullptr ? p.seq[at.b] : at.b;
             const int pg = pos / p.page_size;
             if (row >= 0 && row < p.num_seqs && pg < p.width) {
                 const int page = p.table[row * p.table_stride + pg];
                 if (page >= 0 && page < p.num_pages) {
                     stored = true;
                     const int64_t off = (page * p.c_sp + (pos - pg * p.page_size) * p.c_st) * kElem;
-                    kdst = p.kc + off;
-                    vdst = p.vc + off;
+                    k_out = p.kc + off;
+                    v_out = p.vc + off;
                 }
             }
         }
-        dst_sh = p.c_sh * kElem;
+        out_sh = p.c_sh * kElem;
     } else {
-        kdst = p.ko.ptr + (b * p.ko.sb + n * p.ko.sn) * 2;
-        dst_sh = p.ko.sh * 2;
+        k_out = p.ko.ptr + (at.b * p.ko.sb + at.n * p.ko.sn) * 2;
+        out_sh = p.ko.sh * 2;
     }
 
-    float A[8], Bc[8];
-    if (lo < p.H) {
-        coefficients<D, kNorm, kInter>(my_cs, role, c, p.rot, p.wq, p.w32, 1.f, A, Bc);
-        turn_heads<D, kNorm, kInter, false>(
-            p.q.ptr + (b * p.q.sb + n * p.q.sn) * 2, p.q.sh * 2,
-            p.qo.ptr + (b * p.qo.sb + n * p.qo.sn) * 2, p.qo.sh * 2, lo, min(hi, p.H), h_off,
-            h_step, live, write, c, role, A, Bc, p.eps);
-    }
-    const int k_lo = max(lo - p.H, 0), k_hi = min(hi - p.H, p.H_kv);
-    if (k_lo < k_hi) {
-        coefficients<D, kNorm, kInter>(my_cs, role, c, p.rot, p.wk, p.w32,
-                                       kStore == kPageE4m3 ? p.k_inv : 1.f, A, Bc);
-        turn_heads<D, kNorm, kInter, kStore == kPageE4m3>(
-            p.k.ptr + (b * p.k.sb + n * p.k.sn) * 2, p.k.sh * 2, kdst, dst_sh, k_lo, k_hi, h_off,
-            h_step, live, stored, c, role, A, Bc, p.eps);
-    }
-    if constexpr (kStore != kDense) {
-        const int v_lo = max(lo - p.H - p.H_kv, 0), v_hi = hi - p.H - p.H_kv;
-        const uint8_t* vin = p.v.ptr + (b * p.v.sb + n * p.v.sn) * 2;
-        for (int h0 = v_lo; h0 < v_hi; h0 += h_step * kRotUnroll) {
-            uint4 u[kRotUnroll];
+    for (bool loaded = true; input < (kStore == kDense ? 2 : 3); ++input) {
+        const int size = input == 0 ? p.H : p.H_kv;
+        const int h_lo = max(lo - before, 0), h_hi = min(hi - before, size);
+        before += size;
+        if (h_lo >= h_hi) continue;
+        LaneAngles t;
+        if (input < 2)
+            coefficients<D, kNorm, kInter>(cs + ts * (p.rot >> 1), role, input == 0 ? p.wq : p.wk,
+                                           p.w32, kStore == kPageE4m3 && input == 1 ? p.k_inv : 1.f,
+                                           t);
+        const bool keep = input == 0 ? write : stored;
+        const int64_t sh = input == 0 ? p.qo.sh * 2 : out_sh;
+        uint8_t* row = (input == 0 ? p.qo.ptr + (at.b * p.qo.sb + at.n * p.qo.sn) * 2
+                        : input == 1 ? k_out : v_out) + (h_lo + h_off) * sh;
+        const bool codes = kStore == kPageE4m3 && input != 0;            // uniform
+        for (int h0 = h_lo; h0 < h_hi; h0 += h_step * kRotUnroll) {
+            if (!loaded) load(input, h0, h_hi, u);
+            loaded = false;
 #pragma unroll
             for (int i = 0; i < kRotUnroll; ++i) {
-                const int h = h0 + i * h_step + h_off;
-                if (stored && h < v_hi)
-                    u[i] = *reinterpret_cast<const uint4*>(vin + h * p.v.sh * 2 + c * 16);
-            }
+                if (h0 + i * h_step >= h_hi) break;          // uniform in the block
+                const bool here = keep && h0 + i * h_step + h_off < h_hi;
+                f2 x0[4], x1[4], y0[4], y1[4];
+                unpack8(u[i][0], x0);
+                unpack8(u[i][1], x1);
+                if (kStore != kDense && input == 2) {
+                    const f2 inv = f2_make(p.v_inv, p.v_inv);
 #pragma unroll
-            for (int i = 0; i < kRotUnroll; ++i) {
-                const int h = h0 + i * h_step + h_off;
-                if (!(stored && h < v_hi)) continue;
-                if constexpr (kStore == kPageE4m3) {
-                    float y[8];
-                    unpack8(u[i], y);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) y[e] *= p.v_inv;
-                    store_chunk<true>(vdst + h * dst_sh, c, y);
+                    for (int j = 0; j < 4; ++j) {
+                        y0[j] = f2_mul(inv, x0[j]);
+                        y1[j] = f2_mul(inv, x1[j]);
+                    }
                 } else {
-                    *reinterpret_cast<uint4*>(vdst + h * dst_sh + c * 16) = u[i];
+                    f2 p0[4], p1[4];
+                    lane_partners<kInter>(x0, x1, part && pass, p0, p1);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        y0[j] = f2_fma(t.a0[j], x0[j], f2_mul(t.b0[j], p0[j]));
+                        y1[j] = f2_fma(t.a1[j], x1[j], f2_mul(t.b1[j], p1[j]));
+                    }
+                    if constexpr (kNorm) {
+                        f2 s2 = f2_mul(x0[0], x0[0]), s3 = f2_mul(x1[0], x1[0]);
+#pragma unroll
+                        for (int j = 1; j < 4; ++j) {
+                            s2 = f2_fma(x0[j], x0[j], s2);
+                            s3 = f2_fma(x1[j], x1[j], s3);
+                        }
+                        const float r = rsqrtf(
+                            fmaf(row_sum<C::kLanes>(f2_sum(s2) + f2_sum(s3)), 1.f / D, p.eps));
+                        const f2 rr = f2_make(r, r);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            y0[j] = f2_mul(y0[j], rr);
+                            y1[j] = f2_mul(y1[j], rr);
+                        }
+                    }
                 }
+                if (here) {
+                    if (codes) {
+                        store_chunk<true>(row, role.c0, y0);
+                        store_chunk<true>(row, role.c1, y1);
+                    } else if ((kStore != kDense && input == 2) || (!kNorm && part && pass)) {
+                        // values, and what is not turned, pass through bit for bit
+                        *reinterpret_cast<uint4*>(row + role.c0 * 16) = u[i][0];
+                        *reinterpret_cast<uint4*>(row + role.c1 * 16) = u[i][1];
+                    } else {
+                        store_chunk<false>(row, role.c0, y0);
+                        store_chunk<false>(row, role.c1, y1);
+                    }
+                }
+                row += h_step * sh;
             }
         }
     }
@@ -382,157 +470,207 @@ __global__ void __launch_bounds__(kRotThreads) fa_qk_rotary_fwd(const RotParams 
 //     dw_e  += g_e x_e r,        dx_e = r (g_e w_e - x_e r^2 mean(g w x)).
 // x is read again (the forward keeps nothing), both row sums are reduced in
 // the same shuffles, and dw is kept in registers over everything a thread
-// sees: its chunk is fixed. The grid is at most kRotBwdBlocks blocks that
-// take (token tile, head split) items in turn, so dw leaves as that many
-// partial rows, which fa_rotary_dw adds in block order: no atomics.
-constexpr int kRotBwdBlocks = 4 * 148;
-constexpr int kRotBwdUnroll = 2;
+// sees: its chunk is fixed. Blocks [0, q_blocks) have
+// q's rows, the others k's, kRotBwdBlocks at most in all (three an SM); dw leaves as that many partial rows, which fa_rotary_dw
+// adds in block order: no atomics.
+// A side's work is its token tiles times its heads, laid end to end in steps of
+// the heads that a block takes at once and shared out evenly. A thread has
+// kRotBwdDepth - 1 rows of g and x under way by cp.async into slots of its own
+// in shared memory, across tiles; no other thread reads them, so no barrier is
+// needed but around the angles. (With two rows in registers instead 52 us for
+// the 43 of B2 H16 N4096 d128, and 123 for 103 at B4 H32 H_kv8.)
+constexpr int kRotBwdBlocks = 3 * 148;
+constexpr int kRotBwdDepth = 5;
+
+struct RotBwdSide {                  // q's or k's
+    RotRows g, x, out;               // output gradient, forward input, gradient
+    const void* w;
+    int heads;
+    uint32_t per_tile;               // steps of a tile's heads
+    int64_t steps;                   // of all tiles
+};
 
 struct RotBwdParams {
-    RotParams f;                     // q, k: the forward's inputs; qo, ko: the outputs dq, dk
-    RotRows dq_out, dk_out;
-    float* part;                     // [blocks][2 D]
-    int64_t items;                   // token tiles * splits
+    RotParams f;                     // tokens, positions, frequencies
+    RotBwdSide side[2];
+    int q_blocks;
+    float* part;                     // [blocks][D]
+};
+
+// A place in the line of steps: token tile and step within it.
+struct RotCursor {
+    uint32_t tile, s;
+    __device__ __forceinline__ bool next(uint32_t per_tile) {            // true: a new tile
+        if (++s < per_tile) return false;
+        s = 0;
+        ++tile;
+        return true;
+    }
 };
 
 template <int D, bool kInter>
-__device__ __forceinline__ void turn_back_heads(const uint8_t* gin, int64_t g_sh,
-                                                const uint8_t* xin, int64_t x_sh, uint8_t* out,
-                                                int64_t out_sh, int h_lo, int h_hi, int h_off,
-                                                int h_step, bool live, int c,
-                                                const ChunkRole& role, const float (&co)[8],
-                                                const float (&si)[8], const void* wp, int w32,
-                                                float eps, float (&dw)[8]) {
-    float w[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = norm_weight(wp, w32, c * 8 + e);
-    for (int h0 = h_lo; h0 < h_hi; h0 += h_step * kRotBwdUnroll) {
-        uint4 gu[kRotBwdUnroll], xu[kRotBwdUnroll];
-#pragma unroll
-        for (int i = 0; i < kRotBwdUnroll; ++i) {
-            const int h = h0 + i * h_step + h_off;
-            gu[i] = xu[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (live && h < h_hi) {
-                gu[i] = *reinterpret_cast<const uint4*>(gin + h * g_sh + c * 16);
-                xu[i] = *reinterpret_cast<const uint4*>(xin + h * x_sh + c * 16);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kRotBwdUnroll; ++i) {
-            if (h0 + i * h_step >= h_hi) break;              // uniform in the block
-            const int h = h0 + i * h_step + h_off;
-            float x[8], g[8], gp[8];
-            unpack8(xu[i], x);
-            unpack8(gu[i], g);
-            chunk_partners<kInter>(gu[i], role, gp);
-            float ss = 0.f, dot = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                g[e] = fmaf(co[e], g[e], si[e] * gp[e]);
-                ss = fmaf(x[e], x[e], ss);
-                dot = fmaf(g[e] * w[e], x[e], dot);
-            }
-#pragma unroll
-            for (int off = D / 16; off > 0; off >>= 1) {
-                ss += __shfl_xor_sync(0xffffffffu, ss, off);
-                dot += __shfl_xor_sync(0xffffffffu, dot, off);
-            }
-            const float r = rsqrtf(fmaf(ss, 1.f / D, eps));
-            const float k = r * r * dot * (1.f / D);
-            if (live && h < h_hi) {                          // others hold zeros or no row
-                float y[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    dw[e] = fmaf(g[e], x[e] * r, dw[e]);
-                    y[e] = r * fmaf(g[e], w[e], -x[e] * k);
-                }
-                *reinterpret_cast<uint4*>(out + h * out_sh + c * 16) = pack8(y);
-            }
-        }
-    }
-}
-
-template <int D, bool kInter>
-__global__ void __launch_bounds__(kRotThreads) fa_qk_rotary_bwd_norm(const RotBwdParams bp) {
+__global__ void __launch_bounds__(kRotThreads, kRotBwdBlocks / 148)
+    fa_qk_rotary_bwd_norm(const RotBwdParams bp) {
     using C = RotCfg<D>;
     const RotParams& p = bp.f;
+    __shared__ __align__(16) uint4 ring[kRotBwdDepth][4][kRotThreads];   // g, g, x, x
     __shared__ __align__(16) float2 cs[C::kTable];           // then the dw reduction, 8 KB both
     static_assert(C::kTable * 2 == C::kSlots * D, "the reduction reuses the table");
     pdl_launch_dependents();
-    const int tid = threadIdx.x, lane = tid & 31;
+    const int tid = threadIdx.x;
     const int tt = 1 << p.tt_shift;
-    const int c = tid % C::kLanes, slot = tid / C::kLanes;
+    const int slot = tid / C::kLanes;
     const int ts = slot & (tt - 1), h_off = slot >> p.tt_shift, h_step = C::kSlots >> p.tt_shift;
-    const ChunkRole role = chunk_role<D, kInter>(c, lane, p.rot);
-    const int heads = p.H + p.H_kv;
-    float dwq[8], dwk[8];
+    const LaneRole role = lane_role<kInter>(tid % C::kLanes, p.rot);
+    const bool zero = p.rot < D && !role.turned;
+    const bool for_k = (int)blockIdx.x >= bp.q_blocks;
+    const RotBwdSide& sd = bp.side[for_k ? 1 : 0];
+    const int64_t blk = blockIdx.x - (for_k ? bp.q_blocks : 0);
+    const int64_t blks = for_k ? gridDim.x - bp.q_blocks : bp.q_blocks;
+    const uint32_t first = (uint32_t)(blk * sd.steps / blks);
+    const int count = (int)((uint32_t)((blk + 1) * sd.steps / blks) - first);
+    f2 w0[4], w1[4], dw0[4], dw1[4];
+    norm_weights(sd.w, p.w32, role.c0, w0);
+    norm_weights(sd.w, p.w32, role.c1, w1);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) dwq[e] = dwk[e] = 0.f;
+    for (int j = 0; j < 4; ++j) dw0[j] = dw1[j] = f2_make(0.f, 0.f);
 
-    for (int64_t item = blockIdx.x; item < bp.items; item += gridDim.x) {
-        const int64_t tile = item / p.splits;
-        const int split = (int)(item - tile * p.splits);
-        const int64_t tok0 = tile * tt;
-        const int lo = (int)((int64_t)heads * split / p.splits);
-        const int hi = (int)((int64_t)heads * (split + 1) / p.splits);
-        __syncthreads();                                     // the last item's table is read
-        rotary_table(cs, p, tok0, tt, tid);
-        __syncthreads();
-        const int64_t tok = tok0 + ts;
-        const bool live = tok < p.tokens;
-        const int64_t b = live ? tok / p.N : 0, n = live ? tok - b * p.N : 0;
-        float co[8], si[8];
-        chunk_angles<kInter>(cs + ts * (p.rot >> 1), role, co, si);
-        if (lo < p.H)
-            turn_back_heads<D, kInter>(
-                bp.dq_out.ptr + (b * bp.dq_out.sb + n * bp.dq_out.sn) * 2, bp.dq_out.sh * 2,
-                p.q.ptr + (b * p.q.sb + n * p.q.sn) * 2, p.q.sh * 2,
-                p.qo.ptr + (b * p.qo.sb + n * p.qo.sn) * 2, p.qo.sh * 2, lo, min(hi, p.H), h_off,
-                h_step, live, c, role, co, si, p.wq, p.w32, p.eps, dwq);
-        const int k_lo = max(lo - p.H, 0), k_hi = hi - p.H;
-        if (k_lo < k_hi)
-            turn_back_heads<D, kInter>(
-                bp.dk_out.ptr + (b * bp.dk_out.sb + n * bp.dk_out.sn) * 2, bp.dk_out.sh * 2,
-                p.k.ptr + (b * p.k.sb + n * p.k.sn) * 2, p.k.sh * 2,
-                p.ko.ptr + (b * p.ko.sb + n * p.ko.sn) * 2, p.ko.sh * 2, k_lo, k_hi, h_off,
-                h_step, live, c, role, co, si, p.wk, p.w32, p.eps, dwk);
+    // past a tile's last token the batch's first stands in, unused
+    auto token_at = [&](uint32_t tile, RotToken* t0) {
+        const int64_t tok0 = (int64_t)tile << p.tt_shift;
+        *t0 = rot_token(p, tok0);
+        RotToken at{t0->b, t0->n + ts};
+        if (tok0 + ts >= p.tokens) at = RotToken{0, 0};
+        else if (at.n >= p.N) at = rot_token(p, tok0 + ts);
+        return at;
+    };
+    RotCursor put{first / sd.per_tile, first % sd.per_tile};
+    RotCursor get = put;
+    int put_i = 0;
+    const uint8_t *g_in = nullptr, *x_in = nullptr;
+    auto enter = [&]() {
+        RotToken t0;
+        const RotToken at = token_at(put.tile, &t0);
+        g_in = sd.g.ptr + (at.b * sd.g.sb + at.n * sd.g.sn) * 2;
+        x_in = sd.x.ptr + (at.b * sd.x.sb + at.n * sd.x.sn) * 2;
+    };
+    if (count > 0) enter();
+    auto issue = [&](int at_slot) {
+        if (put_i < count) {
+            const int h = min((int)put.s * h_step + h_off, sd.heads - 1);
+            const uint8_t *gr = g_in + h * sd.g.sh * 2, *xr = x_in + h * sd.x.sh * 2;
+            cp_async16(smem_u32(&ring[at_slot][0][tid]), gr + role.c0 * 16, true);
+            cp_async16(smem_u32(&ring[at_slot][1][tid]), gr + role.c1 * 16, true);
+            cp_async16(smem_u32(&ring[at_slot][2][tid]), xr + role.c0 * 16, true);
+            cp_async16(smem_u32(&ring[at_slot][3][tid]), xr + role.c1 * 16, true);
+            ++put_i;
+            if (put.next(sd.per_tile) && put_i < count) enter();
+        }
+        cp_async_commit();
+    };
+    for (int i = 0; i < kRotBwdDepth - 1; ++i) issue(i);
+
+    bool fresh = true, live = false;
+    LaneAngles t;
+    uint8_t* out = nullptr;
+    for (int i = 0, from = 0; i < count; ++i) {
+        if (fresh) {
+            RotToken t0;
+            const RotToken at = token_at(get.tile, &t0);
+            const int64_t tok0 = (int64_t)get.tile << p.tt_shift;
+            live = tok0 + ts < p.tokens;
+            out = sd.out.ptr + (at.b * sd.out.sb + at.n * sd.out.sn) * 2;
+            if (i > 0) __syncthreads();                      // the last tile's angles are read
+            rotary_table(cs, p, tok0, t0, tt, tid);
+            __syncthreads();
+            lane_angles<kInter>(cs + ts * (p.rot >> 1), role, t);
+        }
+        issue(from == 0 ? kRotBwdDepth - 1 : from - 1);      // where the row before this lay
+        const int h = (int)get.s * h_step + h_off;
+        cp_async_wait<kRotBwdDepth - 1>();
+        {
+            f2 x0[4], x1[4], g0[4], g1[4], p0[4], p1[4];
+            unpack8(ring[from][0][tid], g0);
+            unpack8(ring[from][1][tid], g1);
+            unpack8(ring[from][2][tid], x0);
+            unpack8(ring[from][3][tid], x1);
+            lane_partners<kInter>(g0, g1, zero, p0, p1);
+            f2 s2 = 0ull, s3 = 0ull, d2 = 0ull, d3 = 0ull;
+            f2 y0[4], y1[4];                                 // g w, then dx
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                g0[j] = turn2<kInter>(t.a0[j], g0[j], t.b0[j], p0[j]);
+                g1[j] = turn2<kInter>(t.a1[j], g1[j], t.b1[j], p1[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                y0[j] = f2_mul(g0[j], w0[j]);
+                y1[j] = f2_mul(g1[j], w1[j]);
+                s2 = f2_fma(x0[j], x0[j], s2);
+                s3 = f2_fma(x1[j], x1[j], s3);
+                d2 = f2_fma(y0[j], x0[j], d2);
+                d3 = f2_fma(y1[j], x1[j], d3);
+            }
+            float ss = f2_sum(s2) + f2_sum(s3), dot = f2_sum(d2) + f2_sum(d3);
+#pragma unroll
+            for (int off = C::kLanes / 2; off > 0; off >>= 1) {
+                ss += __shfl_xor_sync(0xffffffffu, ss, off);
+                dot += __shfl_xor_sync(0xffffffffu, dot, off);
+            }
+            const float r = rsqrtf(fmaf(ss, 1.f / D, p.eps));
+            const float k = -r * r * r * dot * (1.f / D);
+            if (live && h < sd.heads) {
+                const f2 rr = f2_make(r, r), kk = f2_make(k, k);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    dw0[j] = f2_fma(f2_mul(g0[j], rr), x0[j], dw0[j]);
+                    dw1[j] = f2_fma(f2_mul(g1[j], rr), x1[j], dw1[j]);
+                    y0[j] = f2_fma(y0[j], rr, f2_mul(x0[j], kk));
+                    y1[j] = f2_fma(y1[j], rr, f2_mul(x1[j], kk));
+                }
+                uint8_t* row = out + h * sd.out.sh * 2;
+                *reinterpret_cast<uint4*>(row + role.c0 * 16) = pack8(y0);
+                *reinterpret_cast<uint4*>(row + role.c1 * 16) = pack8(y1);
+            }
+        }
+        from = from + 1 == kRotBwdDepth ? 0 : from + 1;
+        fresh = get.next(sd.per_tile);
     }
+    cp_async_wait<0>();
 
     float* red = reinterpret_cast<float*>(cs);               // [kSlots][D]
-    auto reduce = [&](const float (&dw)[8], float* dst) {
-        __syncthreads();
+    __syncthreads();
 #pragma unroll
-        for (int e = 0; e < 8; e += 4)
-            *reinterpret_cast<float4*>(red + slot * D + c * 8 + e) =
-                make_float4(dw[e], dw[e + 1], dw[e + 2], dw[e + 3]);
-        __syncthreads();
-        for (int j = tid; j < D; j += kRotThreads) {
-            float s = 0.f;
-            for (int r = 0; r < C::kSlots; ++r) s += red[r * D + j];
-            dst[j] = s;
-        }
-    };
-    reduce(dwq, bp.part + (int64_t)blockIdx.x * 2 * D);
-    reduce(dwk, bp.part + (int64_t)blockIdx.x * 2 * D + D);
+    for (int j = 0; j < 4; ++j) {
+        *reinterpret_cast<float2*>(red + slot * D + role.c0 * 8 + 2 * j) = f2_get(dw0[j]);
+        *reinterpret_cast<float2*>(red + slot * D + role.c1 * 8 + 2 * j) = f2_get(dw1[j]);
+    }
+    __syncthreads();
+    for (int j = tid; j < D; j += kRotThreads) {
+        float s = 0.f;
+        for (int r = 0; r < C::kSlots; ++r) s += red[r * D + j];
+        bp.part[(int64_t)blockIdx.x * D + j] = s;
+    }
 }
 
-// dw[j] = sum over blocks of part[block][j], j < 2 D: 32 columns a block, 32
-// rows of threads, in fp64 and a fixed order.
+// dw[j] = sum over the side's blocks of part[block][j]: 32 columns a block, 32
+// rows of threads, in fp64 and a fixed order. blockIdx.y 0: q, 1: k.
 template <int D>
 __global__ void __launch_bounds__(1024)
-    fa_rotary_dw(const float* part, int blocks, float* dwq, float* dwk) {
+    fa_rotary_dw(const float* part, int blocks, int q_blocks, float* dwq, float* dwk) {
     pdl_wait_prerequisites();
     __shared__ double red[32][33];
     const int j = blockIdx.x * 32 + threadIdx.x;
+    const int lo = blockIdx.y ? q_blocks : 0, hi = blockIdx.y ? blocks : q_blocks;
     double s = 0.0;
-    for (int r = threadIdx.y; r < blocks; r += 32) s += (double)part[(int64_t)r * 2 * D + j];
+    for (int r = lo + (int)threadIdx.y; r < hi; r += 32) s += (double)part[(int64_t)r * D + j];
     red[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
     if (threadIdx.y == 0) {
         double t = 0.0;
 #pragma unroll
         for (int r = 0; r < 32; ++r) t += red[r][threadIdx.x];
-        (j < D ? dwq[j] : dwk[j - D]) = (float)t;
+        (blockIdx.y ? dwk : dwq)[j] = (float)t;
     }
 }
 

@@ -22,6 +22,8 @@ inline void rot_fill(RotParams* p, const fa_rotary_t& r, const int32_t* pos, int
     p->wk = r.k_weight;
     p->w32 = r.weight_f32;
     p->rot = r.rotary_dim;
+    p->pair_shift = 0;
+    while ((1 << p->pair_shift) < r.rotary_dim / 2) ++p->pair_shift;
     p->cs_scale = r.rotary_scale;
     p->sin_sign = 1.f;
     p->eps = r.norm_eps;
@@ -32,22 +34,30 @@ inline void rot_fill(RotParams* p, const fa_rotary_t& r, const int32_t* pos, int
     p->tokens = (int64_t)B * N;
 }
 
-// How the rows go to blocks. A block holds `slots` rows at a time; it takes
-// as many tokens as it has slots (fewer where the batch has fewer tokens, the
+// Tokens of a tile, and the tiles: a block holds `slots` rows at a time; it
+// takes as many tokens as it has slots (fewer where the batch has fewer, the
 // slots then spread over heads), so that a thread's angles serve all its
-// heads. The heads of a token tile are split over blocks only until there are
-// kRotFill blocks (4 an SM): each split computes the tile's angles again.
-constexpr int64_t kRotFill = 4 * 148;
-
-inline int64_t rot_tiling(RotParams* p, int slots, int heads) {
+// heads.
+inline int64_t rot_tiles(RotParams* p, int slots) {
     int shift = 0;
     while ((1 << shift) < slots && ((int64_t)1 << shift) < p->tokens) ++shift;
     p->tt_shift = shift;
-    const int64_t tiles = (p->tokens + (1ll << shift) - 1) >> shift;
-    const int step = slots >> shift;                         // heads a block takes at once
-    const int64_t most = (heads + step - 1) / step;
-    p->splits = (int)std::max<int64_t>(1, std::min<int64_t>(most, (kRotFill + tiles - 1) / tiles));
-    return tiles * p->splits;
+    return (p->tokens + (1ll << shift) - 1) >> shift;
+}
+
+// Steps of `heads` heads in a tile: as many heads as a block takes at once.
+inline int rot_steps(const RotParams& p, int slots, int heads) {
+    const int step = slots >> p.tt_shift;
+    return (heads + step - 1) / step;
+}
+
+// The grid of a forward or an append: token tiles, their heads split over
+// blocks (each of which computes the tile's angles) up to kRotFill blocks.
+inline unsigned rot_grid(RotParams* p, int slots, int heads) {
+    const int64_t tiles = rot_tiles(p, slots);
+    p->splits = (int)std::max<int64_t>(1, std::min<int64_t>(rot_steps(*p, slots, heads),
+                                                            (kRotFill + tiles - 1) / tiles));
+    return (unsigned)(tiles * p->splits);
 }
 
 // Positions: a device array that stays inside 63 bits of address.

