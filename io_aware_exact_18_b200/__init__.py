@@ -401,5 +401,16 @@ def decode_attention_fp8(q8, k8, v8, q_descale, k_descale, v_descale, scale=None
     return out, lse
 
 
-from .paged import copy_pages, paged_append, paged_decode_attention  # noqa: E402
-from .rotary import qk_rotary, qk_rotary_bwd, rotary_frequencies  # noqa: E402
+# Bindings that import torch, on first use.
+_TORCH_BINDINGS = {"qk_rotary": "rotary", "qk_rotary_bwd": "rotary", "rotary_frequencies": "rotary",
+                   "paged_append": "paged", "paged_decode_attention": "paged",
+                   "copy_pages": "paged"}
+
+
+def __getattr__(name):
+    if name not in _TORCH_BINDINGS:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    import importlib
+    value = getattr(importlib.import_module("." + _TORCH_BINDINGS[name], __name__), name)
+    globals()[name] = value
+    return value

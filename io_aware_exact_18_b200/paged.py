@@ -12,8 +12,11 @@ from __future__ import annotations
 import math
 import struct
 
-from .rotary import (HEADS, NO_HEADS, ROTARY, _failed, heads_of, on_device, positions_of,
-                     rotary_of)
+import torch
+
+from . import FA_OK, FAError, load_library
+from ._marshal import (BF16, E4M3, F32, HEADS, I32, NO_HEADS, ROTARY, four, heads_of, on,
+                       positions_of, rotary_of, stream_of, vector_of, workspace_of)
 
 # fa_paged_cache_t: two pointers, three strides, five int32, two floats, int32;
 # fa_block_table_t: pointer, stride, two int32 (include/fa_paged.h)
@@ -26,15 +29,14 @@ _COPY = struct.Struct("@" + CACHE)
 
 def cache_of(k_cache, v_cache, k_descale, v_descale):
     """fa_paged_cache_t fields of the two page tensors."""
-    import torch
     dt = k_cache.dtype
-    if dt == torch.bfloat16:
+    if dt is BF16:
         elem = 2
-    elif dt == torch.float8_e4m3fn:
+    elif dt is E4M3:
         elem = 1
     else:
         raise TypeError("cache pages must be bfloat16 or float8_e4m3fn")
-    if v_cache.dtype != dt:
+    if v_cache.dtype is not dt:
         raise TypeError("K and V pages must have one type")
     if not k_cache.is_cuda or v_cache.device != k_cache.device:
         raise ValueError("K and V pages must be on one CUDA device (no CPU fallback)")
@@ -42,30 +44,20 @@ def cache_of(k_cache, v_cache, k_descale, v_descale):
     st = k_cache.stride()
     if len(s) != 4 or v_cache.shape != s or v_cache.stride() != st or st[3] != 1:
         raise ValueError("K and V pages: [pages, H_kv, page_size, d] views with equal strides "
-                         f"and a contiguous last axis expected, got {tuple(s)} {st} and "
-                         f"{tuple(v_cache.shape)} {v_cache.stride()}")
+                         f"and a contiguous last axis expected, got {list(s)} {st} and "
+                         f"{list(v_cache.shape)} {v_cache.stride()}")
     return (k_cache.data_ptr(), v_cache.data_ptr(), st[0], st[1], st[2], s[0], s[2], s[1], s[3],
-            elem, float(k_descale), float(v_descale), 0)
+            elem, k_descale, v_descale, 0)
 
 
 def table_of(block_table, device):
     """fa_block_table_t fields."""
-    import torch
-    if block_table.dtype != torch.int32 or block_table.device != device or \
-            block_table.dim() != 2 or (block_table.shape[1] > 1 and block_table.stride(1) != 1):
-        raise ValueError("block_table must be int32 [sequences, pages] on the cache's device, "
+    s = block_table.shape
+    if block_table.dtype is not I32 or block_table.device != device or len(s) != 2 or \
+            (s[1] > 1 and block_table.stride(1) != 1):
+        raise ValueError(f"block_table must be int32 [sequences, pages] on {device}, "
                          "rows contiguous")
-    return (block_table.data_ptr(), block_table.stride(0), block_table.shape[0],
-            block_table.shape[1])
-
-
-def _int32_vector(t, what, n, device):
-    import torch
-    if t.dtype != torch.int32 or t.device != device or t.dim() != 1 or \
-            (n is not None and t.shape[0] != n) or not t.is_contiguous():
-        raise ValueError(f"{what} must be a contiguous int32 vector"
-                         f"{'' if n is None else f' [{n}]'} on the cache's device")
-    return t.data_ptr()
+    return block_table.data_ptr(), block_table.stride(0), s[0], s[1]
 
 
 def paged_append(k, v, k_cache, v_cache, block_table, positions, q=None, freqs=None,
@@ -80,35 +72,37 @@ def paged_append(k, v, k_cache, v_cache, block_table, positions, q=None, freqs=N
     :func:`qk_rotary` (norm_eps, k_weight, freqs; both None: stored as they
     come), and so is q [B, H, N, d] if given, into q_out (allocated unless
     given; may be q). e4m3 pages hold value / descale, saturated. Tokens with a
-    negative position are padding: nothing of them is written. Tokens whose
-    page the table does not give are dropped from the cache.
+    negative position are padding: nothing of them is written, and an allocated
+    q_out holds arbitrary values in their rows. Tokens whose page the table does
+    not give are dropped from the cache. Two tokens of a call must not go to the
+    same slot.
     """
-    import torch
-    from . import FA_OK, load_library
     cache = cache_of(k_cache, v_cache, k_descale, v_descale)
     dev, H_kv, d = k_cache.device, cache[7], cache[8]
-    B, N = k.shape[0], k.shape[-2]
-    kh, vh = heads_of(k, "k", B, H_kv, N, d), heads_of(v, "v", B, H_kv, N, d)
-    qh, H = NO_HEADS, 0
-    if q is not None:
-        qh, H = heads_of(q, "q", B, None, N, d), q.shape[1]
-    for t in (k, v, q, q_out):
-        if t is not None and t.device != dev:
-            raise ValueError("all tensors must be on the cache's device")
+    B, _, N, _ = four(k, "k")
+    ks = (B, H_kv, N, d)
+    kh, vh = heads_of(k, "k", ks, dev), heads_of(v, "v", ks, dev)
     table = table_of(block_table, dev)
     pos = positions_of(positions, B, N, dev)
-    sp = 0 if seq is None else _int32_vector(seq, "seq", B, dev)
+    sp = 0 if seq is None else vector_of(seq, "seq", B, dev)
     rot = rotary_of(freqs, interleaved, rotary_scale, norm_eps, q_weight, k_weight, d, dev)
-    with on_device(dev, stream) as s:
-        oh = NO_HEADS
+    qh = oh = NO_HEADS
+    H = 0
+    with on(dev, stream):
         if q is not None:
+            H = four(q, "q")[1]
+            qs = (B, H, N, d)
+            qh = heads_of(q, "q", qs, dev)
             if q_out is None:
-                q_out = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=dev)
-            oh = heads_of(q_out, "q_out", B, H, N, d)
+                q_out = torch.empty(B, H, N, d, dtype=BF16, device=dev)
+            oh = heads_of(q_out, "q_out", qs, dev)
+        elif q_out is not None:
+            raise ValueError("q_out is given, but no q")
         st = load_library().fa_paged_append(
-            _APPEND.pack(*cache, *table, *kh, *vh, *qh, *oh, *pos, sp, *rot, B, H, N, 0), s)
+            _APPEND.pack(*cache, *table, *kh, *vh, *qh, *oh, *pos, sp, *rot, B, H, N, 0),
+            stream_of(dev, stream))
     if check and st != FA_OK:
-        _failed(st, "fa_paged_append")
+        raise FAError(st, "fa_paged_append")
     return q_out
 
 
@@ -122,41 +116,34 @@ def paged_decode_attention(q, k_cache, v_cache, block_table, kv_len, scale=None,
     allocated with torch unless given as a CUDA uint8 tensor of at least
     fa_paged_decode_workspace_bytes(B, H, H_kv, d) bytes.
     """
-    import torch
-    from . import FA_OK, load_library
     cache = cache_of(k_cache, v_cache, k_descale, v_descale)
     dev, d = k_cache.device, cache[8]
-    qh = heads_of(q, "q", q.shape[0], None, 1, d)
-    B, H = q.shape[0], q.shape[1]
-    for t in (q, out, lse, workspace):
-        if t is not None and t.device != dev:
-            raise ValueError("all tensors must be on the cache's device")
+    B, H, _, _ = four(q, "q")
+    qs = (B, H, 1, d)
+    qp, qsb, qsh, _ = heads_of(q, "q", qs, dev)
     table = table_of(block_table, dev)
-    lens = _int32_vector(kv_len, "kv_len", B, dev)
+    lens = vector_of(kv_len, "kv_len", B, dev)
     if scale is None:
         scale = 1.0 / math.sqrt(d)
     lib = load_library()
-    with on_device(dev, stream) as s:
+    with on(dev, stream):
         if out is None:
-            out = torch.empty((B, H, 1, d), dtype=torch.bfloat16, device=dev)
-        elif out.dtype != torch.bfloat16 or tuple(out.shape) != (B, H, 1, d) or \
+            out = torch.empty(B, H, 1, d, dtype=BF16, device=dev)
+        elif out.dtype is not BF16 or out.shape != qs or out.device != dev or \
                 not out.is_contiguous():
-            raise ValueError(f"out must be a contiguous bfloat16 [{B}, {H}, 1, {d}]")
+            raise ValueError(f"out must be a contiguous bfloat16 {list(qs)} on {dev}")
         if lse is None:
-            lse = torch.empty((B, H, 1), dtype=torch.float32, device=dev)
-        elif lse.dtype != torch.float32 or tuple(lse.shape) != (B, H, 1) or \
+            lse = torch.empty(B, H, 1, dtype=F32, device=dev)
+        elif lse.dtype is not F32 or lse.shape != qs[:3] or lse.device != dev or \
                 not lse.is_contiguous():
-            raise ValueError(f"lse must be a contiguous float32 [{B}, {H}, 1]")
-        need = lib.fa_paged_decode_workspace_bytes(B, H, cache[7], d)
-        if workspace is None and need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        ws, ws_bytes = (None, 0) if workspace is None else \
-            (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+            raise ValueError(f"lse must be a contiguous float32 {list(qs[:3])} on {dev}")
+        ws, ws_bytes, workspace = workspace_of(
+            workspace, lib.fa_paged_decode_workspace_bytes(B, H, cache[7], d), dev)
         st = lib.fa_paged_decode(
-            _DECODE.pack(*cache, *table, qh[0], qh[1], qh[2], out.data_ptr(), lse.data_ptr(),
-                         lens, B, H, float(scale), 0), ws, ws_bytes, s)
+            _DECODE.pack(*cache, *table, qp, qsb, qsh, out.data_ptr(), lse.data_ptr(), lens, B, H,
+                         scale, 0), ws, ws_bytes, stream_of(dev, stream))
     if check and st != FA_OK:
-        _failed(st, "fa_paged_decode")
+        raise FAError(st, "fa_paged_decode")
     return out, lse
 
 
@@ -165,13 +152,11 @@ def copy_pages(k_cache, v_cache, src, dst, stream=None, check=True):
     copy-on-write forks and for compaction. Pages may be read several times; no
     dst may appear twice or among src (src[i] == dst[i] changes nothing). Pairs
     with a page outside the cache are skipped."""
-    from . import FA_OK, load_library
     cache = cache_of(k_cache, v_cache, 1.0, 1.0)
     dev = k_cache.device
-    sp = _int32_vector(src, "src", None, dev)
-    n = src.shape[0]
-    dp = _int32_vector(dst, "dst", n, dev)
-    with on_device(dev, stream) as s:
-        st = load_library().fa_copy_pages(_COPY.pack(*cache), sp, dp, n, s)
+    n = src.numel()
+    sp, dp = vector_of(src, "src", n, dev), vector_of(dst, "dst", n, dev)
+    with on(dev, stream):
+        st = load_library().fa_copy_pages(_COPY.pack(*cache), sp, dp, n, stream_of(dev, stream))
     if check and st != FA_OK:
-        _failed(st, "fa_copy_pages")
+        raise FAError(st, "fa_copy_pages")

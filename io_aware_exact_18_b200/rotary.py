@@ -9,13 +9,14 @@ from __future__ import annotations
 import math
 import struct
 
-# fa_heads_t: pointer and three strides; fa_rotary_t: three pointers, four
-# int32, two floats (include/fa_rotary.h)
-HEADS = "Pqqq"
-ROTARY = "PPPiiiiff"
+import torch
+
+from . import FA_OK, FAError, load_library
+from ._marshal import (BF16, F32, HEADS, NO_HEADS, ROTARY, device_of, four, heads_of, on,
+                       positions_of, rotary_of, stream_of, workspace_of)
+
 _QK = struct.Struct("@" + 4 * HEADS + "Pqq" + ROTARY + "6i")
 _QK_BWD = struct.Struct("@" + 6 * HEADS + "Pqq" + ROTARY + "PP" + "6i")
-NO_HEADS = (0, 0, 0, 0)
 
 
 def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0,
@@ -32,7 +33,6 @@ def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0,
       stay, those that turn at most `low` times are divided by factor, and those
       between are blended linearly in their number of turns.
     """
-    import torch
     r = int(rotary_dim)
     if r < 0 or r % 16 != 0:
         raise ValueError(f"rotary_dim must be a multiple of 16, got {rotary_dim}")
@@ -55,100 +55,6 @@ def rotary_frequencies(rotary_dim, base=10000.0, scaling=None, factor=1.0,
     return f.to(device)
 
 
-def heads_of(t, what, B=None, heads=None, N=None, d=None):
-    """fa_heads_t fields of a bf16 CUDA [B, heads, N, d] view (any strides but
-    a contiguous last axis), its sizes checked where given."""
-    import torch
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{what} must be bfloat16")
-    if not t.is_cuda:
-        raise ValueError(f"{what} must be a CUDA tensor (no CPU fallback)")
-    s = t.shape
-    if len(s) != 4 or (B is not None and (s[0] != B or s[2] != N or s[3] != d)) or \
-            (heads is not None and s[1] != heads):
-        want = [B, heads, N, d] if B is not None else "[B, heads, N, d]"
-        raise ValueError(f"{what}: {want} expected, got {tuple(s)}")
-    st = t.stride()
-    if st[3] != 1:
-        raise ValueError(f"{what}: the last axis must be contiguous")
-    return t.data_ptr(), st[0], st[1], st[2]
-
-
-def positions_of(positions, B, N, device):
-    """Pointer and strides of int32 CUDA positions [B, N] (or [N], repeated)."""
-    import torch
-    if positions.dtype != torch.int32 or positions.device != device:
-        raise ValueError("positions must be int32 on the device of q and k")
-    if positions.dim() == 1 and positions.shape[0] == N:
-        return positions.data_ptr(), 0, positions.stride(0)
-    if tuple(positions.shape) != (B, N):
-        raise ValueError(f"positions: [{B}, {N}] or [{N}] expected, got "
-                         f"{tuple(positions.shape)}")
-    st = positions.stride()
-    return positions.data_ptr(), st[0], st[1]
-
-
-def rotary_of(freqs, interleaved, rotary_scale, norm_eps, q_weight, k_weight, d, device):
-    """fa_rotary_t fields."""
-    import torch
-    fp, r = 0, 0
-    if freqs is not None:
-        if freqs.dtype != torch.float64 or freqs.device != device or freqs.dim() != 1 or \
-                not freqs.is_contiguous():
-            raise ValueError("freqs must be a contiguous fp64 vector on the device of q and k")
-        fp, r = freqs.data_ptr(), 2 * freqs.shape[0]
-    qw = kw = w32 = 0
-    if q_weight is not None or k_weight is not None:
-        if norm_eps is None:
-            raise ValueError("norm weights are given, but no norm_eps")
-        kinds = set()
-        for w in (q_weight, k_weight):
-            if w is None:
-                continue
-            if w.device != device or tuple(w.shape) != (d,) or not w.is_contiguous():
-                raise ValueError(f"norm weights must be contiguous [{d}] on the device of q and k")
-            kinds.add(w.dtype)
-        if kinds == {torch.float32}:
-            w32 = 1
-        elif kinds != {torch.bfloat16}:
-            raise TypeError("norm weights must be both bfloat16 or both float32")
-        qw = 0 if q_weight is None else q_weight.data_ptr()
-        kw = 0 if k_weight is None else k_weight.data_ptr()
-    return (fp, qw, kw, r, int(bool(interleaved)), int(norm_eps is not None), w32,
-            float(rotary_scale), 0.0 if norm_eps is None else float(norm_eps))
-
-
-class on_device:
-    """The context of a call: the tensors' device made current, and, where the
-    caller names a stream, torch's allocations made for that stream."""
-
-    def __init__(self, device, stream):
-        import torch
-        self.guards = []
-        if device.index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(device))
-        if stream is not None:
-            self.guards.append(torch.cuda.stream(
-                torch.cuda.ExternalStream(int(stream), device=device)))
-        self.device, self.stream = device, stream
-
-    def __enter__(self):
-        import torch
-        for g in self.guards:
-            g.__enter__()
-        return self.stream if self.stream is not None else \
-            torch.cuda.current_stream(self.device).cuda_stream
-
-    def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
-
-
-def _failed(status, what):
-    from . import FAError
-    raise FAError(status, what)
-
-
 def qk_rotary(q, k, positions, freqs, interleaved=False, rotary_scale=1.0, norm_eps=None,
               q_weight=None, k_weight=None, q_out=None, k_out=None, stream=None, check=True):
     """q_out, k_out = norm (if norm_eps is given) and rotary position of bf16
@@ -161,26 +67,24 @@ def qk_rotary(q, k, positions, freqs, interleaved=False, rotary_scale=1.0, norm_
     ones. Outputs are allocated contiguous unless given; an output may be its
     input.
     """
-    import torch
-    from . import FA_OK, load_library
-    qh = heads_of(q, "q")
-    B, H, N, d = q.shape
-    kh = heads_of(k, "k", B, None, N, d)
-    if k.device != q.device:
-        raise ValueError("q and k must be on one device")
-    rot = rotary_of(freqs, interleaved, rotary_scale, norm_eps, q_weight, k_weight, d, q.device)
-    pos = positions_of(positions, B, N, q.device)
-    with on_device(q.device, stream) as s:
+    dev = device_of(q, "q")
+    qs, ks = four(q, "q"), four(k, "k")
+    B, H, N, d = qs
+    H_kv = ks[1]
+    qh, kh = heads_of(q, "q", qs, dev), heads_of(k, "k", (B, H_kv, N, d), dev)
+    rot = rotary_of(freqs, interleaved, rotary_scale, norm_eps, q_weight, k_weight, d, dev)
+    pos = positions_of(positions, B, N, dev)
+    with on(dev, stream):
         if q_out is None:
-            q_out = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=q.device)
+            q_out = torch.empty(B, H, N, d, dtype=BF16, device=dev)
         if k_out is None:
-            k_out = torch.empty((B, k.shape[1], N, d), dtype=torch.bfloat16, device=q.device)
+            k_out = torch.empty(B, H_kv, N, d, dtype=BF16, device=dev)
         st = load_library().fa_qk_rotary(
-            _QK.pack(*qh, *kh, *heads_of(q_out, "q_out", B, H, N, d),
-                     *heads_of(k_out, "k_out", B, k.shape[1], N, d), *pos, *rot,
-                     B, H, k.shape[1], N, d, 0), s)
+            _QK.pack(*qh, *kh, *heads_of(q_out, "q_out", qs, dev),
+                     *heads_of(k_out, "k_out", ks, dev), *pos, *rot, B, H, H_kv, N, d, 0),
+            stream_of(dev, stream))
     if check and st != FA_OK:
-        _failed(st, "fa_qk_rotary")
+        raise FAError(st, "fa_qk_rotary")
     return q_out, k_out
 
 
@@ -194,45 +98,39 @@ def qk_rotary_bwd(dq_out, dk_out, q, k, positions, freqs, interleaved=False, rot
     fp32 [d], summed over batch, heads and tokens (given for absent weights
     too). Without one, q and k may be None and the weight gradients are None.
     """
-    import torch
-    from . import FA_OK, load_library
-    gq = heads_of(dq_out, "dq_out")
-    B, H, N, d = dq_out.shape
-    gk = heads_of(dk_out, "dk_out", B, None, N, d)
-    H_kv, dev = dk_out.shape[1], dq_out.device
+    dev = device_of(dq_out, "dq_out")
+    qs, ks = four(dq_out, "dq_out"), four(dk_out, "dk_out")
+    B, H, N, d = qs
+    H_kv = ks[1]
+    gq = heads_of(dq_out, "dq_out", qs, dev)
+    gk = heads_of(dk_out, "dk_out", (B, H_kv, N, d), dev)
     norm = norm_eps is not None
     if norm:
         if q is None or k is None:
             raise ValueError("the norm's backward needs q and k")
-        xq, xk = heads_of(q, "q", B, H, N, d), heads_of(k, "k", B, H_kv, N, d)
+        xq, xk = heads_of(q, "q", qs, dev), heads_of(k, "k", ks, dev)
     else:
         xq = xk = NO_HEADS
-    for t in (dk_out, q, k):
-        if t is not None and t.device != dev:
-            raise ValueError("all tensors must be on one device")
     rot = rotary_of(freqs, interleaved, rotary_scale, norm_eps, q_weight, k_weight, d, dev)
     pos = positions_of(positions, B, N, dev)
     lib = load_library()
-    with on_device(dev, stream) as s:
+    with on(dev, stream):
         if dq is None:
-            dq = torch.empty((B, H, N, d), dtype=torch.bfloat16, device=dev)
+            dq = torch.empty(B, H, N, d, dtype=BF16, device=dev)
         if dk is None:
-            dk = torch.empty((B, H_kv, N, d), dtype=torch.bfloat16, device=dev)
-        dw, wp, ws_bytes = (None, None), (0, 0), 0
+            dk = torch.empty(B, H_kv, N, d, dtype=BF16, device=dev)
+        dwq = dwk = None
+        pwq = pwk = need = 0
         if norm:
-            both = torch.empty((2, d), dtype=torch.float32, device=dev)
-            dw = (both[0], both[1])
-            wp = (dw[0].data_ptr(), dw[1].data_ptr())
+            dwq = torch.empty(d, dtype=F32, device=dev)
+            dwk = torch.empty(d, dtype=F32, device=dev)
+            pwq, pwk = dwq.data_ptr(), dwk.data_ptr()
             need = lib.fa_qk_rotary_bwd_workspace_bytes(B, H, H_kv, N, d, 1)
-            if workspace is None and need > 0:
-                workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        if workspace is not None:
-            ws_bytes = workspace.numel() * workspace.element_size()
+        ws, ws_bytes, workspace = workspace_of(workspace, need, dev)
         st = lib.fa_qk_rotary_bwd(
-            _QK_BWD.pack(*gq, *gk, *xq, *xk, *heads_of(dq, "dq", B, H, N, d),
-                         *heads_of(dk, "dk", B, H_kv, N, d), *pos, *rot, *wp,
-                         B, H, H_kv, N, d, 0),
-            None if workspace is None else workspace.data_ptr(), ws_bytes, s)
+            _QK_BWD.pack(*gq, *gk, *xq, *xk, *heads_of(dq, "dq", qs, dev),
+                         *heads_of(dk, "dk", ks, dev), *pos, *rot, pwq, pwk,
+                         B, H, H_kv, N, d, 0), ws, ws_bytes, stream_of(dev, stream))
     if check and st != FA_OK:
-        _failed(st, "fa_qk_rotary_bwd")
-    return dq, dk, dw[0], dw[1]
+        raise FAError(st, "fa_qk_rotary_bwd")
+    return dq, dk, dwq, dwk
