@@ -6,9 +6,10 @@ at most e = scale d 2^-23 sum |q_i k_i| (each addition by one unit, truncating),
 and each exponential by 2^-21 relative besides. lse is then off by at most
 e + 2^-20 plus the fp32 sums' chains (under 2^12 additions a thread, then trees):
 2^-12 at the very worst, in practice far less; the bound takes 2^-17 for chains
-under 2^7. The weights are off by the rounding of p, u = 2^-8 (bf16) or 2^-11
-(f16), e and 2^-21, in numerator and normaliser: O by twice that times
-sum w |v - O|. f16 probabilities under 2^-14 are off by 2^-25 each instead:
+under 2^7. The weights are off by the rounding of p, u = 2^-16 (two bf16 parts,
+half a step 2^-8 of the rest, itself at most 2^-8 of p) or 2^-11 (f16), e and
+2^-21: O by twice that times sum w |v - O|. bf16 divides by the sum of the exact
+p: u sum w |v| more. f16 probabilities under 2^-14 are off by 2^-25 each instead:
 sum |v - O| / sum exp. The fp32 sums of O add 2^-17 sum w |v|, the last rounding
 2^-8 |O|. Append: see tests/test_rotary_gpu.py; an e4m3 code is off by half a
 step, 2^-4 of the value or 2^-10 among subnormals."""
@@ -53,9 +54,11 @@ def decode_and_check(fa, q, kc, vc, ks, vs, table, lens, what="", scale=None, **
     lerr = np.abs(gl[~empty] - rl[~empty])
     assert np.all(lerr <= (e + 2.0 ** -20 + 2.0 ** -17)[~empty] + U * np.abs(rl[~empty])), \
         f"{what}: lse {lerr.max()}"
-    u = 2.0 ** -8 if kc.dtype == torch.bfloat16 else 2.0 ** -11
+    u = 2.0 ** -16 if kc.dtype == torch.bfloat16 else 2.0 ** -11
     tol = 2 * (u + e[..., None] + 2.0 ** -21) * x["dev"] + 2.0 ** -17 * x["absv"] \
         + 2.0 ** -8 * np.abs(ro) + TINY
+    if kc.dtype == torch.bfloat16:
+        tol = tol + u * x["absv"]
     if kc.dtype != torch.bfloat16:
         tol = tol + 2.0 ** -24 * x["flat"]
     err = np.abs(go - ro)
@@ -524,3 +527,95 @@ def test_streams_and_graphs(fa):  # noqa: F811
         decode_and = step()
         assert torch.equal(o, decode_and[0]) and torch.equal(lse, decode_and[1])
         kv_len.copy_(n)
+
+
+def test_empty_calls(fa):  # noqa: F811
+    """No sequences, no tokens, no heads, no pages to copy, no pages at all."""
+    kc, vc, _, _ = pages_of(4, 2, 16, 64, 2, seed=1)
+    k0, v0 = kc.clone(), vc.clone()
+    none = torch.zeros(0, dtype=torch.int32, device=DEV)
+    table = torch.zeros(1, 4, dtype=torch.int32, device=DEV)
+    o, lse = fa.paged_decode_attention(queries(0, 4, 64), kc, vc, table[:0], none)
+    assert o.shape == (0, 4, 1, 64) and lse.shape == (0, 4, 1)
+    x = torch.zeros(1, 2, 0, 64, dtype=torch.bfloat16, device=DEV)
+    fa.paged_append(x, x, kc, vc, table, none[None])
+    fa.copy_pages(kc, vc, none, none)
+    assert torch.equal(kc, k0) and torch.equal(vc, v0)
+    o, lse = fa.paged_decode_attention(queries(1, 4, 64), kc[:0], vc[:0], table,
+                                       torch.tensor([9], dtype=torch.int32, device=DEV))
+    assert (o == 0).all() and torch.isneginf(lse).all()
+    o, lse = fa.paged_decode_attention(queries(1, 4, 64), kc, vc, table[:, :0],
+                                       torch.tensor([9], dtype=torch.int32, device=DEV))
+    assert (o == 0).all() and torch.isneginf(lse).all()
+
+
+def test_decode_shared_table_rows(fa):  # noqa: F811
+    """One table row for all sequences (stride 0), pages listed twice."""
+    kc, vc, _, _ = pages_of(6, 2, 16, 128, 2, seed=2)
+    row = torch.tensor([3, 1, 3, 5], dtype=torch.int32, device=DEV)
+    lens = torch.tensor([64, 10, 33], dtype=torch.int32, device=DEV)
+    decode_and_check(fa, queries(3, 4, 128), kc, vc, 1.0, 1.0, row.expand(3, 4), lens)
+
+
+def test_append_in_place_queries(fa):  # noqa: F811
+    """q_out is q: the same bits as into a new tensor; keys alone without q."""
+    x = torch.randn(3, 12, 5, 128, device=DEV).to(torch.bfloat16)
+    kc, vc, _, _ = pages_of(20, 2, 16, 128, 2, seed=3)
+    k2, v2 = kc.clone(), vc.clone()
+    table = shuffled_table(20, 3, 4)
+    pos = torch.arange(5, dtype=torch.int32, device=DEV)
+    kw = dict(freqs=fa.rotary_frequencies(128), norm_eps=1e-6)
+    q = x[:, :8].clone()
+    want = fa.paged_append(x[:, 8:10], x[:, 10:], kc, vc, table, pos, q=q, **kw)
+    got = fa.paged_append(x[:, 8:10], x[:, 10:], k2, v2, table, pos, q=q, q_out=q, **kw)
+    assert got is q and torch.equal(q, want) and torch.equal(kc, k2) and torch.equal(vc, v2)
+    k2.zero_()
+    assert fa.paged_append(x[:, 8:10], x[:, 10:], k2, v2, table, pos, **kw) is None
+    used = table[:, :1].long()
+    assert torch.equal(k2[used, :, :5], kc[used, :, :5])
+
+
+def test_decode_two_streams_at_once(fa):  # noqa: F811
+    """Calls in flight together on two streams, each with its own workspace."""
+    kc, vc, _, _ = pages_of(1200, 2, 16, 128, 2, seed=4)
+    table = shuffled_table(1200, 4, 300)
+    lens = [torch.tensor(x, dtype=torch.int32, device=DEV)
+            for x in ([4800, 100, 4000, 1], [7, 4700, 0, 2500])]
+    qs = [queries(4, 16, 128, seed=s) for s in (1, 2)]
+    want = [fa.paged_decode_attention(q, kc, vc, table, n) for q, n in zip(qs, lens)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(fa.paged_decode_attention(qs[i], kc, vc, table, lens[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for o, lse in got[i]:
+            assert torch.equal(o, want[i][0]) and torch.equal(lse, want[i][1])
+
+
+N_CASES = 40
+
+
+@pytest.mark.parametrize("case", range(N_CASES))
+def test_random_decoding(fa, case):  # noqa: F811
+    """Seeded random shapes: heads, head dim, page size and order, type, lengths."""
+    rng = np.random.default_rng(1009 + 7919 * case)
+    d = int(rng.choice([64, 128, 256]))
+    H_kv = int(rng.integers(1, 5))
+    H = H_kv * int(rng.choice([1, 2, 3, 4, 7, 8, 12, 16, 18]))
+    page = int(rng.choice([1, 2, 5, 8, 16, 16, 32, 48, 64, 100, 256]))
+    elem = int(rng.choice([1, 2]))
+    B = int(rng.choice([1, 2, 3, 7, 33]))
+    most = int(rng.choice([1, 30, 300, 2000])) if B < 33 else 90
+    lens = rng.integers(0, most + 1, B).astype(np.int32)
+    width = -(-most // page)
+    P = B * width + 1
+    kc, vc, ks, vs = pages_of(P, H_kv, page, d, elem, bool(rng.integers(2)), seed=case,
+                              mult=float(rng.choice([0.25, 1.0, 3.0])))
+    decode_and_check(fa, queries(B, H, d, seed=case, mult=float(rng.choice([0.5, 1.0, 4.0]))),
+                     kc, vc, ks, vs, shuffled_table(P, B, width, seed=case),
+                     torch.from_numpy(lens).to(DEV),
+                     f"case {case}: B{B} H{H} H_kv{H_kv} d{d} page{page} elem{elem} {lens.tolist()}")

@@ -322,3 +322,49 @@ def test_with_attention(fa):
         assert err <= 4e-2 * want.abs().max().item(), f"{name}: {err}"
     err = (o.double() - oo).abs().max().item()
     assert err <= 2e-2 + 2.0 ** -8 * oo.abs().max().item()
+
+
+def test_backward_in_place_and_repeated_gradients(fa):
+    """dq, dk in the place of dq_out, dk_out; output gradients that are one row
+    repeated (strides 0, as a sum's gradient comes); positions one row for all."""
+    B, H, H_kv, N, d = 3, 5, 2, 21, 128
+    q, k = make(B, H, H_kv, N, d, seed=40, fused=True)
+    pos = torch.arange(7, 7 + N, dtype=torch.int32, device=DEV)
+    freqs = fa.rotary_frequencies(96)
+    wq, wk = weights(d, True)
+    row = torch.randn(d, generator=torch.Generator().manual_seed(41)).to(torch.bfloat16).to(DEV)
+    for kw in (dict(norm_eps=1e-6, q_weight=wq, k_weight=wk), dict()):
+        gq, gk = row.expand(B, H, N, d), row.expand(B, H_kv, N, d)
+        got = fa.qk_rotary_bwd(gq, gk, q, k, pos, freqs, **kw)
+        want = fa.qk_rotary_bwd(gq.contiguous(), gk.contiguous(), q, k,
+                                pos.expand(B, N).contiguous(), freqs, **kw)
+        gq, gk = gq.contiguous(), gk.contiguous()
+        place = fa.qk_rotary_bwd(gq, gk, q, k, pos, freqs, dq=gq, dk=gk, **kw)
+        assert place[0] is gq and place[1] is gk
+        for a, b, c in zip(got, want, place):
+            assert (a is None and b is None and c is None) or \
+                (torch.equal(a, b) and torch.equal(a, c))
+
+
+@pytest.mark.parametrize("norm", [None, 1e-6])
+def test_gradient_by_differences(fa, norm):
+    """The backward against differences of the forward itself: along a random
+    direction, (f(x + h v) - f(x - h v)) / 2h from the fp64 oracle's forward at
+    the same bf16 point, whose step errors (1e-10) are far below the bound of the
+    kernel's own rounding: 2^-8 of sum |dx v| for its bf16 result."""
+    B, H, N, d = 1, 2, 6, 64
+    q, k = make(B, H, H, N, d, seed=42)
+    gq, gk = make(B, H, H, N, d, seed=43)
+    pos = torch.arange(100, 100 + N, dtype=torch.int32, device=DEV)
+    freqs = fa.rotary_frequencies(64)
+    dq, dk, _, _ = fa.qk_rotary_bwd(gq, gk, q, k, pos, freqs, norm_eps=norm)
+    p64, f64 = np64(pos)[None], np64(freqs)
+    rng = np.random.default_rng(44)
+    for x, g, dx in ((q, gq, dq), (k, gk, dk)):
+        x, g, dx = np64(x), np64(g), np64(dx)
+        for _ in range(4):
+            v = rng.standard_normal(x.shape)
+            h = 1e-6
+            up = (g * orot.forward(x + h * v, p64, f64, False, 1.0, norm)).sum()
+            down = (g * orot.forward(x - h * v, p64, f64, False, 1.0, norm)).sum()
+            assert abs((up - down) / (2 * h) - (dx * v).sum()) <= 2.0 ** -8 * np.abs(dx * v).sum()
