@@ -268,7 +268,6 @@ int decode(const fa_paged_decode_t& a, void* ws, size_t ws_bytes, void* stream) 
     while ((1ll << lg) < c.page_size) ++lg;
     p.page_mul = (uint32_t)(((1ull << (31 + lg)) + c.page_size - 1) / c.page_size);
     p.page_shift = lg;
-    p.whole16 = c.page_size % 16 == 0;
     p.kv_len = a.kv_len;
     p.o = static_cast<__nv_bfloat16*>(a.o);
     p.lse = a.lse;

@@ -23,13 +23,12 @@
 //
 // A warp has a ring of kStages (K, V) steps of its own that its lanes fill
 // with 16-byte cp.async, and it runs on across unit boundaries: there is no
-// block barrier before the end. Lanes look up the pages of the next step while
-// the present one is computed: where page_size is a multiple of 16, one page
-// for 16 keys, whose rows then follow at a fixed stride; otherwise one key a
-// lane, the row offsets going round by shuffle (measured on the e4m3 batch of
-// 32 ragged sequences of up to 8192 keys: @PAGES@). A key that is hidden or
-// has no page is zero-filled and its score set to -inf, never read, so what
-// lies there cannot reach the result.
+// block barrier before the end. Each lane looks up the page of one key of the
+// next step while the present one is computed, and the rows' offsets go round
+// by shuffle: any page size and page order costs the same (one page looked up
+// for 16 keys, where page_size is a multiple of 16, was no faster). A key that
+// is hidden or has no page is zero-filled and its score set to -inf, never
+// read, so what lies there cannot reach the result.
 //
 // Products (mma.sync m16n8k16, fp32 accumulators): S^T = K Q^T with the keys
 // as rows and 8 query heads as columns, then O^T += V^T P^T. The C fragment of
@@ -87,7 +86,6 @@ struct PdParams {
     int64_t table_stride;
     int width, num_pages, page_size;
     uint32_t page_mul, page_shift;         // key / page_size = (2 key * page_mul) >> 32 >> page_shift
-    int whole16;                           // page_size % 16 == 0: 16 keys share a page
     const int32_t* kv_len;
     __nv_bfloat16* o;
     float* lse;
@@ -178,7 +176,8 @@ __device__ __forceinline__ int seq_len(const PdParams& p, int b) {
 // A place in the line of steps: all sequences for the first unit index (K/V
 // head and block of query heads), then all for the next. Keys of the same
 // tokens are then read for all heads at about the same time, which matters
-// where a token's heads lie side by side (@ORDER@). The next sequence's length
+// where a token's heads lie side by side (e4m3, 32 sequences of 8192 tokens in
+// token-major pages: 104 us with each sequence's heads in turn, 100 so). The next sequence's length
 // is fetched one sequence ahead.
 struct PdCursor {
     int b, unit, step, n, len, next_len;
@@ -274,9 +273,8 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
     PdCursor put = cur;
     int64_t put_i = 0;
     int64_t put_head = (put.unit / p.hblk) * p.c_sh;         // of the unit's K/V head
-    // A lane looks up one key of the next step: its own, or, where pages hold
-    // whole groups of 16 keys, the first of its group.
-    const int lane_key = p.whole16 ? lane & (C::kStep - 16) : lane & (C::kStep - 1);
+    constexpr uint32_t kLanesIn = C::kStep == 32 ? 0xffffffffu : 0xffffu;
+    const int lane_key = lane & (C::kStep - 1);              // a lane looks up its key's page
     int entry = -1, slot_in_page = 0;
     auto lookup = [&]() {
         const int key = put.step * C::kStep + lane_key;
@@ -288,7 +286,6 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
     constexpr int kChunks = C::kRow / 16;                    // of a row
     constexpr int kRowsAt = 32 / kChunks;                    // rows of one warp-wide copy
     const int my_row = lane / kChunks, my_chunk = lane % kChunks;
-    const int64_t lane_off = my_row * p.c_st + my_chunk * 16;
     const int64_t v_off = p.vc - p.kc;
     auto issue = [&](int slot) {
         if (put_i < count) {
@@ -296,46 +293,17 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
             const int64_t off =
                 ok ? entry * p.c_sp + put_head + slot_in_page * p.c_st : 0;
             const uint32_t kd = ring + (uint32_t)(slot * C::kStage), vd = kd + C::kStep * C::kRow;
-            uint32_t mask;
-            if (p.whole16) {
-                // the group's visible keys are its first ones
-                const int left = put.len - (put.step * C::kStep + lane_key);
-                const uint32_t mine16 = ok ? (left >= 16 ? 0xffffu : (1u << left) - 1u) : 0u;
-                mask = mine16;
-                if constexpr (C::kGroups == 2)
-                    mask = __shfl_sync(0xffffffffu, mine16, 0) |
-                           (__shfl_sync(0xffffffffu, mine16, 16) << 16);
-                if (mask != 0) {
+            const uint32_t mask = __ballot_sync(0xffffffffu, ok) & kLanesIn;
+            if (mask != 0) {
+                const uint8_t* base = p.kc + my_chunk * 16;
 #pragma unroll
-                    for (int g = 0; g < C::kGroups; ++g) {
-                        const uint8_t* src = p.kc + lane_off + __shfl_sync(0xffffffffu, off, g * 16);
-#pragma unroll
-                        for (int i = 0; i < 16 / kRowsAt; ++i) {
-                            const int r = g * 16 + i * kRowsAt + my_row;
-                            const bool in = (mask >> r) & 1u;
-                            const uint32_t at = stage_at<C::kRow>(r, my_chunk);
-                            const uint8_t* from = in ? src : p.kc;
-                            cp_async16(kd + at, from, in);
-                            cp_async16(vd + at, from + v_off, in);
-                            src += kRowsAt * p.c_st;
-                        }
-                    }
-                }
-            } else {
-                mask = __ballot_sync(0xffffffffu, ok);
-                if constexpr (C::kGroups == 1) mask &= 0xffffu;
-                if (mask != 0) {
-                    const uint8_t* base = p.kc + my_chunk * 16;
-#pragma unroll
-                    for (int i = 0; i < C::kStep / kRowsAt; ++i) {
-                        const int r = i * kRowsAt + my_row;
-                        const bool in = (mask >> r) & 1u;
-                        const uint8_t* from =
-                            (in ? base : p.kc) + __shfl_sync(0xffffffffu, off, r);
-                        const uint32_t at = stage_at<C::kRow>(r, my_chunk);
-                        cp_async16(kd + at, from, in);
-                        cp_async16(vd + at, from + v_off, in);
-                    }
+                for (int i = 0; i < C::kStep / kRowsAt; ++i) {
+                    const int r = i * kRowsAt + my_row;
+                    const bool in = (mask >> r) & 1u;
+                    const uint8_t* from = (in ? base : p.kc) + __shfl_sync(0xffffffffu, off, r);
+                    const uint32_t at = stage_at<C::kRow>(r, my_chunk);
+                    cp_async16(kd + at, from, in);
+                    cp_async16(vd + at, from + v_off, in);
                 }
             }
             if (lane == 0) my_seen[slot] = mask;
@@ -780,9 +748,11 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
 // loads do not wait for the log-sum-exps. kAt = 8, a block a row, where units
 // are few and have many parts (up to one a block: with one warp a row, parts
 // one after another, the join took 8 us of the 95 of a 131072-key sequence;
-// so, @JOIN@); kAt = 1, rows side by side in a block, from kPdJoinUnits units
-// on, which have at most four parts on average (@JOIN1@).
-constexpr int kPdJoinUnits = 4 * kPdBlocks;
+// so, 3 us); kAt = 1, rows side by side in a block, from kPdJoinUnits units on,
+// which have at most four parts on average (256 sequences of 20 to 300 tokens,
+// 8 K/V heads: 39 us in all, with kAt = 8 53; one sequence of 131072 tokens, 8
+// units: 93 and 90).
+constexpr int kPdJoinUnits = 64;
 
 template <int D, int kAt>
 struct PdJoinCfg {

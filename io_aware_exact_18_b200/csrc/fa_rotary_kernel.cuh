@@ -11,16 +11,15 @@
 // alone, not on the head.
 //
 // What bounds it: HBM, 2 bytes read and 2 written an element (backward with
-// the norm: 4 and 2), and next to it the instructions: some 45 a 16-byte chunk
-// have to fit into the time that its 32 bytes take. So a thread owns two
+// the norm: 4 and 2), and next to it the instructions that a 16-byte
+// chunk takes. So a thread owns two
 // chunks (8 elements each) of the rows of ONE token, keeps their A and B in
 // registers and walks over the heads. In the half layout they are the two
 // chunks whose elements pair up (rotary_dim is a multiple of 16, so whole
 // chunks do), or two neighbours among those that are not turned; interleaved,
 // neighbours. No element crosses lanes then, and fp32 is multiplied in pairs.
 // (With one chunk a thread, the partner's coming by shuffle, unpacked again:
-// 124 instructions a chunk and 62 us where this takes @FWD@, B1 H32 H_kv8
-// N16384 d128 with the norm.) A row's d / 16 lanes lie in one warp, so the sum
+// 124 instructions a chunk where this takes 94.) A row's d / 16 lanes lie in one warp, so the sum
 // of squares is a shuffle reduction.
 //
 // Angles: p f_i is formed in fp64 in turns (f_i / 2 pi), reduced to
