@@ -46,6 +46,14 @@ def heads_of(t, what, shape, device):
     return t.data_ptr(), sb, sh, sn
 
 
+def out_heads(t, what, B, heads, N, d, device):
+    """(tensor, fa_heads_t fields) of a bf16 output: the caller's, or a new one."""
+    if t is not None:
+        return t, heads_of(t, what, (B, heads, N, d), device)
+    t = torch.empty(B, heads, N, d, dtype=BF16, device=device)
+    return t, (t.data_ptr(), heads * N * d, N * d, d)
+
+
 def four(t, what):
     """The shape of a [B, heads, N, d] tensor."""
     s = t.shape
@@ -142,9 +150,12 @@ class _Nothing:
 _NOTHING = _Nothing()
 
 
+_current_device = torch.cuda.current_device
+
+
 def on(device, stream):
     """The context to allocate and launch in."""
-    if stream is None and device.index == torch.cuda.current_device():
+    if stream is None and device.index == _current_device():
         return _NOTHING
     return _Guard(device, stream)
 

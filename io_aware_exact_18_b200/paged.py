@@ -16,7 +16,7 @@ import torch
 
 from . import FA_OK, FAError, load_library
 from ._marshal import (BF16, E4M3, F32, HEADS, I32, NO_HEADS, ROTARY, four, heads_of, on,
-                       positions_of, rotary_of, stream_of, vector_of, workspace_of)
+                       out_heads, positions_of, rotary_of, stream_of, vector_of, workspace_of)
 
 # fa_paged_cache_t: two pointers, three strides, five int32, two floats, int32;
 # fa_block_table_t: pointer, stride, two int32 (include/fa_paged.h)
@@ -91,11 +91,8 @@ def paged_append(k, v, k_cache, v_cache, block_table, positions, q=None, freqs=N
     with on(dev, stream):
         if q is not None:
             H = four(q, "q")[1]
-            qs = (B, H, N, d)
-            qh = heads_of(q, "q", qs, dev)
-            if q_out is None:
-                q_out = torch.empty(B, H, N, d, dtype=BF16, device=dev)
-            oh = heads_of(q_out, "q_out", qs, dev)
+            qh = heads_of(q, "q", (B, H, N, d), dev)
+            q_out, oh = out_heads(q_out, "q_out", B, H, N, d, dev)
         elif q_out is not None:
             raise ValueError("q_out is given, but no q")
         st = load_library().fa_paged_append(

@@ -12,7 +12,7 @@ import struct
 import torch
 
 from . import FA_OK, FAError, load_library
-from ._marshal import (BF16, F32, HEADS, NO_HEADS, ROTARY, device_of, four, heads_of, on,
+from ._marshal import (F32, HEADS, NO_HEADS, ROTARY, device_of, four, heads_of, on, out_heads,
                        positions_of, rotary_of, stream_of, workspace_of)
 
 _QK = struct.Struct("@" + 4 * HEADS + "Pqq" + ROTARY + "6i")
@@ -75,13 +75,10 @@ def qk_rotary(q, k, positions, freqs, interleaved=False, rotary_scale=1.0, norm_
     rot = rotary_of(freqs, interleaved, rotary_scale, norm_eps, q_weight, k_weight, d, dev)
     pos = positions_of(positions, B, N, dev)
     with on(dev, stream):
-        if q_out is None:
-            q_out = torch.empty(B, H, N, d, dtype=BF16, device=dev)
-        if k_out is None:
-            k_out = torch.empty(B, H_kv, N, d, dtype=BF16, device=dev)
+        q_out, oq = out_heads(q_out, "q_out", B, H, N, d, dev)
+        k_out, ok = out_heads(k_out, "k_out", B, H_kv, N, d, dev)
         st = load_library().fa_qk_rotary(
-            _QK.pack(*qh, *kh, *heads_of(q_out, "q_out", qs, dev),
-                     *heads_of(k_out, "k_out", ks, dev), *pos, *rot, B, H, H_kv, N, d, 0),
+            _QK.pack(*qh, *kh, *oq, *ok, *pos, *rot, B, H, H_kv, N, d, 0),
             stream_of(dev, stream))
     if check and st != FA_OK:
         raise FAError(st, "fa_qk_rotary")
@@ -115,10 +112,8 @@ def qk_rotary_bwd(dq_out, dk_out, q, k, positions, freqs, interleaved=False, rot
     pos = positions_of(positions, B, N, dev)
     lib = load_library()
     with on(dev, stream):
-        if dq is None:
-            dq = torch.empty(B, H, N, d, dtype=BF16, device=dev)
-        if dk is None:
-            dk = torch.empty(B, H_kv, N, d, dtype=BF16, device=dev)
+        dq, oq = out_heads(dq, "dq", B, H, N, d, dev)
+        dk, ok = out_heads(dk, "dk", B, H_kv, N, d, dev)
         dwq = dwk = None
         pwq = pwk = need = 0
         if norm:
@@ -128,8 +123,7 @@ def qk_rotary_bwd(dq_out, dk_out, q, k, positions, freqs, interleaved=False, rot
             need = lib.fa_qk_rotary_bwd_workspace_bytes(B, H, H_kv, N, d, 1)
         ws, ws_bytes, workspace = workspace_of(workspace, need, dev)
         st = lib.fa_qk_rotary_bwd(
-            _QK_BWD.pack(*gq, *gk, *xq, *xk, *heads_of(dq, "dq", qs, dev),
-                         *heads_of(dk, "dk", ks, dev), *pos, *rot, pwq, pwk,
+            _QK_BWD.pack(*gq, *gk, *xq, *xk, *oq, *ok, *pos, *rot, pwq, pwk,
                          B, H, H_kv, N, d, 0), ws, ws_bytes, stream_of(dev, stream))
     if check and st != FA_OK:
         raise FAError(st, "fa_qk_rotary_bwd")
