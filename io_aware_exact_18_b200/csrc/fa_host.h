@@ -94,6 +94,21 @@ inline bool same_view(const View& a, const View& b) {
            (a.N <= 1 || a.t.stride_n == b.t.stride_n) && a.H == b.H;
 }
 
+// What a call reads besides its views: nothing it writes may meet them.
+struct ReadSpan {
+    const void* p;
+    size_t n;
+};
+inline ReadSpan positions_span(const int32_t* pos, int64_t sb, int64_t sn, int64_t B, int64_t N) {
+    return ReadSpan{pos, pos == nullptr ? 0 : 4 * (size_t)((B - 1) * sb + (N - 1) * sn + 1)};
+}
+inline ReadSpan freqs_span(const fa_rotary_t& r) {
+    return ReadSpan{r.freqs, (size_t)r.rotary_dim / 2 * 8};
+}
+inline ReadSpan weight_span(const fa_rotary_t& r, const void* w, int d) {
+    return ReadSpan{w, r.norm && w != nullptr ? (size_t)d * (r.weight_f32 ? 4 : 2) : 0};
+}
+
 // Sizes, positions and rotary arguments of the three entry points that turn
 // heads (FA_OK, or the status to return).
 int rotary_check(const fa_rotary_t& r, int d);

@@ -110,6 +110,18 @@ int append(const fa_paged_append_t& a, void* stream) {
     }
     for (const View& x : {k, v, q, qo})
         if (x.H > 0 && meets_cache(c, cbytes, x.t.ptr, view_bytes(x))) return FA_ERR_INVALID_ARG;
+    const int64_t table_ints = a.table.num_seqs == 0 || a.table.pages_per_seq == 0
+                                   ? 0
+                                   : (a.table.num_seqs - 1) * a.table.stride + a.table.pages_per_seq;
+    const ReadSpan reads[6] = {
+        {a.table.pages, (size_t)table_ints * 4}, {a.seq, a.seq ? (size_t)a.B * 4 : 0},
+        positions_span(a.positions, a.pos_stride_b, a.pos_stride_n, a.B, a.N),
+        freqs_span(a.rotary), weight_span(a.rotary, a.rotary.q_weight, c.d),
+        weight_span(a.rotary, a.rotary.k_weight, c.d)};
+    for (const ReadSpan& r : reads)
+        if (meets_cache(c, cbytes, r.p, r.n) ||
+            (H > 0 && bytes_meet(a.q_out.ptr, view_bytes(qo), r.p, r.n)))
+            return FA_ERR_INVALID_ARG;
     int dev = 0;
     rc = device_ready(&dev);
     if (rc != FA_OK) return rc;
@@ -160,7 +172,7 @@ PdPlan pd_plan(int B, int H, int H_kv, int d) {
     pl.G = H / H_kv;
     pl.nt = head_tiles(pl.G);
     pl.hblk = (pl.G + 8 * pl.nt - 1) / (8 * pl.nt);
-    const size_t rows = (size_t)kPdBlocks * 2 * kPdWarpsMost * 8 * pl.nt;
+    const size_t rows = (size_t)kPdBlocks * 2 * pd_warps_most(d, pl.nt) * 8 * pl.nt;
     pl.o_bytes = rows * d * 4;
     pl.lse_bytes = up256(rows * 4);
     pl.split_bytes = up256((size_t)B * H_kv * pl.hblk * 8);

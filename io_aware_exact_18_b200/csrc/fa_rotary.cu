@@ -53,6 +53,18 @@ int views_check(const View* in, int n_in, const View* out, int n_out, const int*
     return FA_OK;
 }
 
+// Outputs against positions, frequencies and weights.
+bool spans_apart(const fa_rotary_t& r, const int32_t* pos, int64_t sb, int64_t sn, int B, int N,
+                 int d, const View* out, int n_out) {
+    const ReadSpan reads[4] = {
+        r.rotary_dim > 0 ? positions_span(pos, sb, sn, B, N) : ReadSpan{nullptr, 0}, freqs_span(r),
+        weight_span(r, r.q_weight, d), weight_span(r, r.k_weight, d)};
+    for (const ReadSpan& x : reads)
+        for (int o = 0; o < n_out; ++o)
+            if (bytes_meet(out[o].t.ptr, view_bytes(out[o]), x.p, x.n)) return false;
+    return true;
+}
+
 template <int D, bool kNorm, bool kInter>
 void launch_fwd_d(RotParams p, unsigned blocks, cudaStream_t s) {
     fa_qk_rotary_fwd<D, kNorm, kInter, kDense><<<blocks, kRotThreads, 0, s>>>(p);
@@ -85,6 +97,8 @@ int fwd(const fa_qk_rotary_t& a, void* stream) {
     const int replaces[2] = {0, 1};
     rc = views_check(in, 2, out, 2, replaces);
     if (rc != FA_OK) return rc;
+    if (!spans_apart(a.rotary, a.positions, a.pos_stride_b, a.pos_stride_n, a.B, a.N, a.d, out, 2))
+        return FA_ERR_INVALID_ARG;
     int dev = 0;
     rc = device_ready(&dev);
     if (rc != FA_OK) return rc;
@@ -178,6 +192,8 @@ int bwd(const fa_qk_rotary_bwd_t& a, void* ws, size_t ws_bytes, void* stream) {
     const int replaces[2] = {0, 1};
     rc = views_check(in, norm ? 4 : 2, out, 2, replaces);
     if (rc != FA_OK) return rc;
+    if (!spans_apart(a.rotary, a.positions, a.pos_stride_b, a.pos_stride_n, a.B, a.N, a.d, out, 2))
+        return FA_ERR_INVALID_ARG;
     const size_t need =
         norm ? (size_t)bwd_blocks_of(a.B, a.H, a.H_kv, a.N, a.d) * a.d * 4 : 0;
     if (norm) {

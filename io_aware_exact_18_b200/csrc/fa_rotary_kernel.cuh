@@ -22,11 +22,13 @@
 // 124 instructions a chunk where this takes 94.) A row's d / 16 lanes lie in one warp, so the sum
 // of squares is a shuffle reduction.
 //
-// Angles: p f_i is formed in fp64 in turns (f_i / 2 pi), reduced to
-// [-1/2, 1/2] there and only then rounded to fp32 (an error of at most 2^-25
-// turns, 2e-7 rad, at any position); fp32 products would be off by 0.01 rad
-// at position 10^5. A block's angles are computed once, cooperatively, into
-// shared memory: a few sincospi a thread for all its heads.
+// Angles: f_i / 2 pi, taken in fp64, becomes a 64-bit fixed-point fraction of a
+// turn, and its product with the position, modulo 2^64, is the angle's fraction
+// of a turn exactly (whole turns fall off the top): 2^-34 turns for any 32-bit
+// position, rounded to fp32 (2^-25 turns, 2e-7 rad) for sincospi. fp32
+// products would be off by 0.01 rad at position 10^5; fp64 products, reduced by
+// rint, cost 1 us a block in conversions. A block's angles are computed once,
+// cooperatively, into shared memory: a few sincospi a thread for all its heads.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -151,21 +153,39 @@ __device__ __forceinline__ RotToken rot_token(const RotParams& p, int64_t tok) {
 }
 
 // (s cos, s sin) of the block's tokens into shared memory (unused past the
-// last token). A thread stays with one pair; (b0, n0) is the first token.
+// last token). A thread stays with one pair and takes kRotAngles tokens at a
+// time, whose chains (position, product, sincospi) then overlap. t0 is the first
+// token.
+constexpr int kRotAngles = 4;
 __device__ __forceinline__ void rotary_table(float2* cs, const RotParams& p, int64_t tok0,
                                              const RotToken& t0, int tt, int tid) {
     const int half = p.rot >> 1, i = tid & ((1 << p.pair_shift) - 1);
     if (i >= half) return;
     const double turn = p.freqs[i] * 0.15915494309189533577;
-    for (int t = tid >> p.pair_shift; t < tt; t += kRotThreads >> p.pair_shift) {
-        if (tok0 + t >= p.tokens) break;
-        RotToken at{t0.b, t0.n + t};
-        if (at.n >= p.N) at = rot_token(p, tok0 + t);
-        double turns = (double)p.pos[at.b * p.pos_sb + at.n * p.pos_sn] * turn;
-        turns -= rint(turns);
-        float c, s;
-        sincospif(2.f * (float)turns, &s, &c);
-        cs[t * half + i] = make_float2(c * p.cs_scale, s * p.cs_scale * p.sin_sign);
+    const uint64_t frac = (uint64_t)((turn - floor(turn)) * 18446744073709551616.0);
+    const int step = kRotThreads >> p.pair_shift;
+    const int n = (int)min((int64_t)tt, p.tokens - tok0);
+    for (int t = tid >> p.pair_shift; t < n; t += step * kRotAngles) {
+        int32_t pos[kRotAngles];
+#pragma unroll
+        for (int k = 0; k < kRotAngles; ++k) {
+            const int tk = min(t + k * step, n - 1);
+            RotToken at{t0.b, t0.n + tk};
+            if (at.n >= p.N) at = rot_token(p, tok0 + tk);
+            pos[k] = p.pos[at.b * p.pos_sb + at.n * p.pos_sn];
+        }
+        float c[kRotAngles], s[kRotAngles];
+#pragma unroll
+        for (int k = 0; k < kRotAngles; ++k) {
+            // the upper half as a signed number: [-1/2, 1/2) turns times 2^32
+            const int32_t part = (int32_t)(((uint64_t)(int64_t)pos[k] * frac) >> 32);
+            sincospif((float)part * 4.656612873077393e-10f, &s[k], &c[k]);   // 2 turns
+        }
+#pragma unroll
+        for (int k = 0; k < kRotAngles; ++k)
+            if (t + k * step < n)
+                cs[(t + k * step) * half + i] =
+                    make_float2(c[k] * p.cs_scale, s[k] * p.cs_scale * p.sin_sign);
     }
 }
 

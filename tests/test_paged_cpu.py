@@ -107,6 +107,10 @@ def append(lib, **over):
     (dict(qo=P + 3 * G), fa.FA_ERR_INVALID_ARG),            # over k
     (dict(qo=P + 5 * G + 256), fa.FA_ERR_INVALID_ARG),      # shifted over q
     (dict(qos=(1024, 0, 128)), fa.FA_ERR_INVALID_ARG),
+    (dict(pos=P + 64), fa.FA_ERR_INVALID_ARG),              # positions in the cache
+    (dict(table=P + G), fa.FA_ERR_INVALID_ARG),
+    (dict(seq=P + 6 * G), fa.FA_ERR_INVALID_ARG),           # under q_out
+    (dict(freqs=P + 6 * G + 8), fa.FA_ERR_INVALID_ARG),
     (dict(B=-1), fa.FA_ERR_INVALID_ARG),
     (dict(N=1 << 30), fa.FA_ERR_INVALID_ARG),
     (dict(B=0), fa.FA_OK),

@@ -103,6 +103,9 @@ BAD = [
     (dict(qo=P + 128), fa.FA_ERR_INVALID_ARG),                 # shifted over its input
     (dict(qo=P + G), fa.FA_ERR_INVALID_ARG),                   # over k
     (dict(ko=P + 2 * G), fa.FA_ERR_INVALID_ARG),               # over the other output
+    (dict(pos=P + 2 * G + 4), fa.FA_ERR_INVALID_ARG),          # read from under an output
+    (dict(freqs=P + 3 * G + 8), fa.FA_ERR_INVALID_ARG),
+    (dict(wk=P + 2 * G), fa.FA_ERR_INVALID_ARG),
     (dict(B=0), fa.FA_OK),
     (dict(N=0, q=0, k=0, qo=0, ko=0), fa.FA_OK),
     (dict(H=0, H_kv=0), fa.FA_OK),
