@@ -7,6 +7,8 @@
 
 #include <cstdint>
 
+#include "sm100_ptx.cuh"
+
 namespace fa {
 
 constexpr int kCopyThreads = 256;
@@ -26,6 +28,8 @@ struct CopyParams {
 
 template <bool kFlat>
 __global__ void __launch_bounds__(kCopyThreads) fa_page_copy(const CopyParams p) {
+    pdl_launch_dependents();
+    pdl_wait_prerequisites();
     uint8_t* base = blockIdx.y ? p.v : p.k;
     const int seg = (int)(blockIdx.x % (unsigned)p.segs);
     const int64_t first = (int64_t)(blockIdx.x / (unsigned)p.segs) * p.per;

@@ -65,23 +65,20 @@ bool meets_cache(const fa_paged_cache_t& c, size_t bytes, const void* p, size_t 
 
 // ------------------------------------------------------------------ append
 template <int D, bool kNorm, bool kInter>
-void launch_append_d(const RotParams& p, unsigned blocks, int elem, cudaStream_t s) {
-    if (elem == 1)
-        fa_qk_rotary_fwd<D, kNorm, kInter, kPageE4m3><<<blocks, kRotThreads, 0, s>>>(p);
-    else
-        fa_qk_rotary_fwd<D, kNorm, kInter, kPageBf16><<<blocks, kRotThreads, 0, s>>>(p);
+int launch_append_d(const RotParams& p, unsigned blocks, int elem, cudaStream_t s) {
+    return launch_dependent(elem == 1 ? fa_qk_rotary_fwd<D, kNorm, kInter, kPageE4m3>
+                                      : fa_qk_rotary_fwd<D, kNorm, kInter, kPageBf16>,
+                            blocks, kRotThreads, 0, s, p);
 }
 
 template <int D>
 int launch_append(RotParams p, int elem, bool norm, bool inter, cudaStream_t s) {
     const unsigned n = rot_grid(&p, RotCfg<D>::kSlots, p.H + 2 * p.H_kv);
     if (norm)
-        inter ? launch_append_d<D, true, true>(p, n, elem, s)
-              : launch_append_d<D, true, false>(p, n, elem, s);
-    else
-        inter ? launch_append_d<D, false, true>(p, n, elem, s)
-              : launch_append_d<D, false, false>(p, n, elem, s);
-    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+        return inter ? launch_append_d<D, true, true>(p, n, elem, s)
+                     : launch_append_d<D, true, false>(p, n, elem, s);
+    return inter ? launch_append_d<D, false, true>(p, n, elem, s)
+                 : launch_append_d<D, false, false>(p, n, elem, s);
 }
 
 int append(const fa_paged_append_t& a, void* stream) {
@@ -182,17 +179,9 @@ PdPlan pd_plan(int B, int H, int H_kv, int d) {
 template <int D, int kAt>
 int launch_join(const PdParams& p, int heads, int warps, cudaStream_t s) {
     using C = PdJoinCfg<D, kAt>;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)(((int64_t)p.B * p.H + C::kRows - 1) / C::kRows));
-    cfg.blockDim = dim3(C::kThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, fa_paged_join<D, kAt>, p, heads, warps);
-    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+    return launch_dependent(fa_paged_join<D, kAt>,
+                            (unsigned)(((int64_t)p.B * p.H + C::kRows - 1) / C::kRows),
+                            C::kThreads, 0, s, p, heads, warps);
 }
 
 template <int D, int E, int NT>
@@ -209,8 +198,8 @@ int launch_decode(const PdParams& p, cudaStream_t s) {
             return FA_ERR_LAUNCH;
         __atomic_store_n(&ready[dev], true, __ATOMIC_RELEASE);
     }
-    kern<<<kPdBlocks, C::kThreads, C::kSmem, s>>>(p);
-    if (cudaGetLastError() != cudaSuccess) return FA_ERR_LAUNCH;
+    const int rc = launch_dependent(kern, kPdBlocks, C::kThreads, C::kSmem, s, p);
+    if (rc != FA_OK) return rc;
     if ((int64_t)p.B * p.H_kv * p.hblk >= kPdJoinUnits)
         return launch_join<D, 1>(p, C::kHeads, C::kWarps, s);
     return launch_join<D, 8>(p, C::kHeads, C::kWarps, s);
@@ -341,9 +330,8 @@ int copy(const fa_paged_cache_t& c, const int32_t* src, const int32_t* dst, int 
     if (rc != FA_OK) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const dim3 grid((unsigned)blocks, 2);
-    if (heads_out || tokens_out) fa_page_copy<true><<<grid, kCopyThreads, 0, s>>>(p);
-    else fa_page_copy<false><<<grid, kCopyThreads, 0, s>>>(p);
-    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+    return launch_dependent(heads_out || tokens_out ? fa_page_copy<true> : fa_page_copy<false>,
+                            grid, kCopyThreads, 0, s, p);
 }
 
 }  // namespace

@@ -234,6 +234,7 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int units = p.H_kv * p.hblk;
     pdl_launch_dependents();
+    pdl_wait_prerequisites();
 
     // ---------------------------------------------------------- the range
     // Steps before each sequence, in every warp by itself (no block barrier
@@ -785,6 +786,7 @@ struct PdJoinCfg {
 template <int D, int kAt>
 __global__ void __launch_bounds__(PdJoinCfg<D, kAt>::kThreads)
     fa_paged_join(const PdParams p, int heads, int warps) {
+    pdl_launch_dependents();
     pdl_wait_prerequisites();
     using C = PdJoinCfg<D, kAt>;
     constexpr int kLanes = C::kLanes;

@@ -66,16 +66,16 @@ bool spans_apart(const fa_rotary_t& r, const int32_t* pos, int64_t sb, int64_t s
 }
 
 template <int D, bool kNorm, bool kInter>
-void launch_fwd_d(RotParams p, unsigned blocks, cudaStream_t s) {
-    fa_qk_rotary_fwd<D, kNorm, kInter, kDense><<<blocks, kRotThreads, 0, s>>>(p);
+int launch_fwd_d(const RotParams& p, unsigned blocks, cudaStream_t s) {
+    return launch_dependent(fa_qk_rotary_fwd<D, kNorm, kInter, kDense>, blocks, kRotThreads, 0, s, p);
 }
 
 template <int D>
 int launch_fwd(RotParams p, bool norm, bool inter, cudaStream_t s) {
     const unsigned n = rot_grid(&p, RotCfg<D>::kSlots, p.H + p.H_kv);
-    if (norm) inter ? launch_fwd_d<D, true, true>(p, n, s) : launch_fwd_d<D, true, false>(p, n, s);
-    else inter ? launch_fwd_d<D, false, true>(p, n, s) : launch_fwd_d<D, false, false>(p, n, s);
-    return cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+    if (norm)
+        return inter ? launch_fwd_d<D, true, true>(p, n, s) : launch_fwd_d<D, true, false>(p, n, s);
+    return inter ? launch_fwd_d<D, false, true>(p, n, s) : launch_fwd_d<D, false, false>(p, n, s);
 }
 
 int launch_fwd_any(const RotParams& p, int d, bool norm, bool inter, cudaStream_t s) {
@@ -144,21 +144,12 @@ int bwd_blocks_of(int B, int H, int H_kv, int N, int d) {
 template <int D>
 int launch_bwd(RotBwdParams bp, bool inter, float* dwq, float* dwk, cudaStream_t s) {
     const int blocks = bwd_blocks(&bp, RotCfg<D>::kSlots);
-    if (inter) fa_qk_rotary_bwd_norm<D, true><<<blocks, kRotThreads, 0, s>>>(bp);
-    else fa_qk_rotary_bwd_norm<D, false><<<blocks, kRotThreads, 0, s>>>(bp);
-    if (cudaGetLastError() != cudaSuccess) return FA_ERR_LAUNCH;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(D / 32, 2);
-    cfg.blockDim = dim3(32, 32);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, fa_rotary_dw<D>, (const float*)bp.part, blocks,
-                                             bp.q_blocks, dwq, dwk);
-    return e == cudaSuccess && cudaGetLastError() == cudaSuccess ? FA_OK : FA_ERR_LAUNCH;
+    const int rc = launch_dependent(
+        inter ? fa_qk_rotary_bwd_norm<D, true> : fa_qk_rotary_bwd_norm<D, false>, blocks,
+        kRotThreads, 0, s, bp);
+    if (rc != FA_OK) return rc;
+    return launch_dependent(fa_rotary_dw<D>, dim3(D / 32, 2), dim3(32, 32), 0, s,
+                            (const float*)bp.part, blocks, bp.q_blocks, dwq, dwk);
 }
 
 int bwd(const fa_qk_rotary_bwd_t& a, void* ws, size_t ws_bytes, void* stream) {

@@ -339,6 +339,8 @@ template <int D, bool kNorm, bool kInter, int kStore>
 __global__ void __launch_bounds__(kRotThreads, kRotBlocksPerSm) fa_qk_rotary_fwd(const RotParams p) {
     using C = RotCfg<D>;
     __shared__ __align__(16) float2 cs[C::kTable];
+    pdl_launch_dependents();
+    pdl_wait_prerequisites();
     const int tid = threadIdx.x;
     const int tt = 1 << p.tt_shift;
     const uint32_t tile = blockIdx.x / (uint32_t)p.splits;
@@ -536,6 +538,7 @@ __global__ void __launch_bounds__(kRotThreads, kRotBwdBlocks / 148)
     __shared__ __align__(16) float2 cs[C::kTable];           // then the dw reduction, 8 KB both
     static_assert(C::kTable * 2 == C::kSlots * D, "the reduction reuses the table");
     pdl_launch_dependents();
+    pdl_wait_prerequisites();
     const int tid = threadIdx.x;
     const int tt = 1 << p.tt_shift;
     const int slot = tid / C::kLanes;
@@ -677,6 +680,7 @@ __global__ void __launch_bounds__(kRotThreads, kRotBwdBlocks / 148)
 template <int D>
 __global__ void __launch_bounds__(1024)
     fa_rotary_dw(const float* part, int blocks, int q_blocks, float* dwq, float* dwk) {
+    pdl_launch_dependents();
     pdl_wait_prerequisites();
     __shared__ double red[32][33];
     const int j = blockIdx.x * 32 + threadIdx.x;

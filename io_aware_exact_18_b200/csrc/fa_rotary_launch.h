@@ -4,6 +4,7 @@
 #include <algorithm>
 
 #include "fa_host.h"
+#include "fa_launch.h"
 #include "fa_rotary_kernel.cuh"
 
 namespace fa {
