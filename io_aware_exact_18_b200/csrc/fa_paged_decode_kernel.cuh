@@ -50,10 +50,10 @@
 // rounded probabilities. lse takes the exact sum.
 //
 // Measured (device time, both kernels): one sequence of 131072 tokens, 8 K/V
-// heads, d 128 90 us (537 MB: 6.0 TB/s), 16 of 2048 to 8192 tokens 61.5 us
-// (336 MB: 5.5 TB/s), 256 of 20 to 300 tokens 39 us (171 MB: 4.4 TB/s), e4m3
-// 32 of 9 to 8192 tokens 58.6 us (269 MB: 4.6 TB/s; all 8192 long, head-major
-// pages, 91 us for 537 MB), 777 tokens 12 heads d 64 8.1 us. Of a long call 4
+// heads, d 128 90 us (537 MB: 6.0 TB/s), 16 of 2048 to 8192 tokens 59.7 us
+// (336 MB: 5.6 TB/s), 256 of 20 to 300 tokens 39 us (171 MB: 4.4 TB/s), e4m3
+// 32 of 9 to 8192 tokens 58.1 us (269 MB: 4.6 TB/s; all 8192 long, head-major
+// pages, 91 us for 537 MB), 777 tokens 12 heads d 64 8.9 us. Of a long call 4
 // us pass before the first key arrives (lengths, page numbers, keys: three
 // trips to memory), and 5 to 9 between the first and the last SM's end: under
 // full load a fifth of the SMs get a tenth less bandwidth.

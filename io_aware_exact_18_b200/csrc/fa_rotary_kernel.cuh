@@ -328,8 +328,8 @@ __device__ __forceinline__ void coefficients(const float2* cs, const LaneRole& r
 // thread goes through its own in batches of kRotUnroll rows (two chunks each)
 // kept on the way in registers, the first batch while the angles are computed.
 // What decides the speed is the bytes on the way: batches of two, three and
-// four rows took 75, 67 and 62 us (B1 H32 H_kv8 N16384 d128 with the norm,
-// 51 us at the copy rate). Tried, and no faster: the work shared out evenly
+// four rows took 75, 67 and 61 us (B1 H32 H_kv8 N16384 d128 with the norm,
+// 51 us at the copy rate; the same walk that only copies the rows, 59 us). Tried, and no faster: the work shared out evenly
 // over one round of blocks (62 us; 1024 tiles over 592 places are two rounds
 // for the work of 1.7), more splits (65 us with two: each computes the angles
 // again), and rows fetched by cp.async up to eight ahead (63 us; interleaved

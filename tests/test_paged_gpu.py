@@ -619,3 +619,50 @@ def test_random_decoding(fa, case):  # noqa: F811
                      kc, vc, ks, vs, shuffled_table(P, B, width, seed=case),
                      torch.from_numpy(lens).to(DEV),
                      f"case {case}: B{B} H{H} H_kv{H_kv} d{d} page{page} elem{elem} {lens.tolist()}")
+
+
+def test_calls_in_a_row_wait_for_one_another(fa):  # noqa: F811
+    """The kernels start before their predecessors end and wait inside: a chain
+    in which each call reads what the one before wrote (torch kernels among
+    them), run without and with a synchronisation after every call."""
+    B, H, H_kv, d, page = 3, 8, 2, 128, 16
+    freqs = fa.rotary_frequencies(128)
+    table = shuffled_table(120, B, 20)
+    spare = torch.tensor([x for x in range(120) if x not in set(table.flatten().tolist())][:B],
+                         dtype=torch.int32, device=DEV)
+    start = torch.randn(B, H + 2 * H_kv, 1, d, device=DEV).to(torch.bfloat16)
+
+    def chain(wait):
+        def step(value):
+            if wait:
+                torch.cuda.synchronize()
+            return value
+
+        kc = torch.zeros(120, H_kv, page, d, dtype=torch.bfloat16, device=DEV)
+        vc = torch.zeros_like(kc)
+        t = table.clone()
+        n = torch.zeros(B, dtype=torch.int32, device=DEV)
+        x = start.clone()
+        outs = []
+        for i in range(60):
+            q = step(fa.paged_append(x[:, H:H + H_kv], x[:, H + H_kv:], kc, vc, t, n[:, None],
+                                     q=x[:, :H], freqs=freqs, norm_eps=1e-6))
+            n = step(n + 1)
+            o, lse = step(fa.paged_decode_attention(q, kc, vc, t, n))
+            if i == 30:                                      # the last pages move away
+                old = t[:, 1].contiguous()
+                step(fa.copy_pages(kc, vc, old, spare))
+                t[:, 1] = step(spare)
+            qr, kr = step(fa.qk_rotary(o, o[:, :H_kv], n[:, None], freqs))
+            dq, dk, dw, _ = step(fa.qk_rotary_bwd(qr, kr, o, o[:, :H_kv], n[:, None], freqs,
+                                                  norm_eps=1e-6))
+            x = step(torch.cat([dq, dk, kr], 1))             # the next token
+            outs.append((o, lse, dw))
+        torch.cuda.synchronize()
+        return outs, kc, vc
+
+    a, b = chain(True), chain(False)
+    assert torch.equal(a[1], b[1]) and torch.equal(a[2], b[2])
+    for u, v in zip(a[0], b[0]):
+        for p, r in zip(u, v):
+            assert torch.equal(p, r)
