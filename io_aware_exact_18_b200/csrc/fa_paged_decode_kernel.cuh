@@ -28,7 +28,10 @@
 // by shuffle: any page size and page order costs the same (one page looked up
 // for 16 keys, where page_size is a multiple of 16, was no faster). A key that
 // is hidden or has no page is zero-filled and its score set to -inf, never
-// read, so what lies there cannot reach the result.
+// read, so what lies there cannot reach the result. Keys and values are read
+// once and marked to leave L2 first: parts, tables and what the next kernels
+// read stay there (without: 60.4 us for 58.6 on a batch of 16, 38.8 for 35.3
+// on one of 256 short sequences).
 //
 // Products (mma.sync m16n8k16, fp32 accumulators): S^T = K Q^T with the keys
 // as rows and 8 query heads as columns, then O^T += V^T P^T. The C fragment of
@@ -50,9 +53,9 @@
 // rounded probabilities. lse takes the exact sum.
 //
 // Measured (device time, both kernels): one sequence of 131072 tokens, 8 K/V
-// heads, d 128 90 us (537 MB: 6.0 TB/s), 16 of 2048 to 8192 tokens 59.7 us
-// (336 MB: 5.6 TB/s), 256 of 20 to 300 tokens 39 us (171 MB: 4.4 TB/s), e4m3
-// 32 of 9 to 8192 tokens 58.1 us (269 MB: 4.6 TB/s; all 8192 long, head-major
+// heads, d 128 89 us (537 MB: 6.1 TB/s), 16 of 2048 to 8192 tokens 57.6 us
+// (336 MB: 5.8 TB/s), 256 of 20 to 300 tokens 35 us (171 MB: 4.9 TB/s), e4m3
+// 32 of 9 to 8192 tokens 54.7 us (269 MB: 4.9 TB/s; all 8192 long, head-major
 // pages, 91 us for 537 MB), 777 tokens 12 heads d 64 8.9 us. Of a long call 4
 // us pass before the first key arrives (lengths, page numbers, keys: three
 // trips to memory), and 5 to 9 between the first and the last SM's end: under
@@ -309,6 +312,7 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
     constexpr int kRowsAt = 32 / kChunks;                    // rows of one warp-wide copy
     const int my_row = lane / kChunks, my_chunk = lane % kChunks;
     const int64_t v_off = p.vc - p.kc;
+    const uint64_t once = policy_evict_first();              // keys and values are read once
     auto issue = [&](int slot) {
         if (put_i < count) {
             const bool ok = entry >= 0 && entry < p.num_pages;
@@ -324,8 +328,8 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
                     const bool in = (mask >> r) & 1u;
                     const uint8_t* from = (in ? base : p.kc) + __shfl_sync(0xffffffffu, off, r);
                     const uint32_t at = stage_at<C::kRow>(r, my_chunk);
-                    cp_async16(kd + at, from, in);
-                    cp_async16(vd + at, from + v_off, in);
+                    cp_async16(kd + at, from, in, once);
+                    cp_async16(vd + at, from + v_off, in, once);
                 }
             }
             if (lane == 0) my_seen[slot] = mask;
