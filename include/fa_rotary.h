@@ -12,8 +12,8 @@
  * with r = rotary_dim <= d, f_i = freqs[i] and s = rotary_scale. Pair i is
  * (y_i, y_{i + r/2}), or (y_{2i}, y_{2i+1}) with interleaved = 1; elements
  * r .. d-1 are not turned (and not scaled by s). Arithmetic is fp32, rounded
- * once to bf16; the angle p f_i is taken in fp64 and reduced to one turn
- * there, so far positions lose nothing.
+ * once to bf16; the angle is a product in 64-bit fixed-point fractions of a
+ * turn, so far positions lose nothing. Frequencies are finite.
  *
  * Conventions are those of fa.h (device pointers owned by the caller, status
  * codes, errors reported before any CUDA call, asynchronous calls,

@@ -63,6 +63,7 @@ def qk_rotary(q, k, positions, freqs, interleaved=False, rotary_scale=1.0, norm_
     positions: int32 [B, N] or [N]. freqs: fp64 [r / 2] radians per position
     (:func:`rotary_frequencies`), or None to norm only; the first r elements of
     each head are turned, in pairs (i, i + r/2) or, interleaved, (2i, 2i + 1).
+    Frequencies must be finite.
     q_weight, k_weight: norm weights [d], both bf16 or both fp32, None for
     ones. Outputs are allocated contiguous unless given; an output may be its
     input.
