@@ -254,8 +254,12 @@ __device__ __forceinline__ f2 turn2(f2 a, f2 x, f2 b, f2 p) {
     return f2_make(fmaf(ca.x, u.x, cb.x * v.x), fmaf(ca.y, u.y, cb.y * v.y));
 }
 
-// The partners' elements. Where `part` of the head is turned, lanes that are
-// not get 0, so that an infinity there is not multiplied by a zero coefficient.
+// The partners' elements. Where part of the head is turned, lanes that are not
+// get `zero`, so that an infinity there is not multiplied by a zero coefficient.
+// (The selects are 16 instructions a row. A branch around the products instead
+// is slower here, 61.4 us for 60.5 in the normed case below: the rows of
+// a batch are then computed one after another. The backward pass, which has one
+// row at a time, gains 2 % from it.)
 template <bool kInter>
 __device__ __forceinline__ void lane_partners(const f2 (&x0)[4], const f2 (&x1)[4], bool zero,
                                               f2 (&p0)[4], f2 (&p1)[4]) {
@@ -499,7 +503,7 @@ __global__ void __launch_bounds__(kRotThreads, kRotBlocksPerSm) fa_qk_rotary_fwd
 // kRotBwdDepth - 1 rows of g and x under way by cp.async into slots of its own
 // in shared memory, across tiles; no other thread reads them, so no barrier is
 // needed but around the angles. (With two rows in registers instead 52 us for
-// the 43 of B2 H16 N4096 d128, and 123 for 103 at B4 H32 H_kv8.)
+// the 41 of B2 H16 N4096 d128, and 123 for 103 at B4 H32 H_kv8.)
 constexpr int kRotBwdBlocks = 3 * 148;
 constexpr int kRotBwdDepth = 5;
 
@@ -544,7 +548,7 @@ __global__ void __launch_bounds__(kRotThreads, kRotBwdBlocks / 148)
     const int slot = tid / C::kLanes;
     const int ts = slot & (tt - 1), h_off = slot >> p.tt_shift, h_step = C::kSlots >> p.tt_shift;
     const LaneRole role = lane_role<kInter>(tid % C::kLanes, p.rot);
-    const bool zero = p.rot < D && !role.turned;
+    const bool alone = p.rot < D && !role.turned;            // no partners: multiplied by 1
     const bool for_k = (int)blockIdx.x >= bp.q_blocks;
     const RotBwdSide& sd = bp.side[for_k ? 1 : 0];
     const int64_t blk = blockIdx.x - (for_k ? bp.q_blocks : 0);
@@ -611,18 +615,21 @@ __global__ void __launch_bounds__(kRotThreads, kRotBwdBlocks / 148)
         const int h = (int)get.s * h_step + h_off;
         cp_async_wait<kRotBwdDepth - 1>();
         {
-            f2 x0[4], x1[4], g0[4], g1[4], p0[4], p1[4];
+            f2 x0[4], x1[4], g0[4], g1[4];
             unpack8(ring[from][0][tid], g0);
             unpack8(ring[from][1][tid], g1);
             unpack8(ring[from][2][tid], x0);
             unpack8(ring[from][3][tid], x1);
-            lane_partners<kInter>(g0, g1, zero, p0, p1);
             f2 s2 = 0ull, s3 = 0ull, d2 = 0ull, d3 = 0ull;
             f2 y0[4], y1[4];                                 // g w, then dx
+            if (!alone) {
+                f2 p0[4], p1[4];
+                lane_partners<kInter>(g0, g1, false, p0, p1);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                g0[j] = turn2<kInter>(t.a0[j], g0[j], t.b0[j], p0[j]);
-                g1[j] = turn2<kInter>(t.a1[j], g1[j], t.b1[j], p1[j]);
+                for (int j = 0; j < 4; ++j) {
+                    g0[j] = turn2<kInter>(t.a0[j], g0[j], t.b0[j], p0[j]);
+                    g1[j] = turn2<kInter>(t.a1[j], g1[j], t.b1[j], p1[j]);
+                }
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
