@@ -152,39 +152,44 @@ __device__ __forceinline__ RotToken rot_token(const RotParams& p, int64_t tok) {
     return RotToken{(int64_t)b, tok - (int64_t)b * p.N};
 }
 
-// (s cos, s sin) of the block's tokens into shared memory (unused past the
-// last token). A thread stays with one pair and takes kRotAngles tokens at a
-// time, whose chains (position, product, sincospi) then overlap. t0 is the first
-// token.
+// A thread's pair among the angles, and its fraction of a turn a position.
+struct RotPair {
+    int i;                           // rot / 2 and more: none
+    uint64_t frac;
+};
+__device__ __forceinline__ RotPair rot_pair(const RotParams& p, int tid) {
+    RotPair r{tid & ((1 << p.pair_shift) - 1), 0};
+    if (r.i < p.rot >> 1) {
+        const double turn = p.freqs[r.i] * 0.15915494309189533577;
+        r.frac = (uint64_t)((turn - floor(turn)) * 18446744073709551616.0);
+    }
+    return r;
+}
+
+// (s cos, s sin) of a tile's n tokens into shared memory. A thread stays with
+// its pair and takes kRotAngles tokens at a time, whose chains (position,
+// product, sincospi) then overlap. position(t) is token t's; all threads call
+// it together.
 constexpr int kRotAngles = 4;
-__device__ __forceinline__ void rotary_table(float2* cs, const RotParams& p, int64_t tok0,
-                                             const RotToken& t0, int tt, int tid) {
-    const int half = p.rot >> 1, i = tid & ((1 << p.pair_shift) - 1);
-    if (i >= half) return;
-    const double turn = p.freqs[i] * 0.15915494309189533577;
-    const uint64_t frac = (uint64_t)((turn - floor(turn)) * 18446744073709551616.0);
-    const int step = kRotThreads >> p.pair_shift;
-    const int n = (int)min((int64_t)tt, p.tokens - tok0);
-    for (int t = tid >> p.pair_shift; t < n; t += step * kRotAngles) {
+template <class Position>
+__device__ __forceinline__ void rotary_table(float2* cs, const RotParams& p, const RotPair& pair,
+                                             int n, int tid, Position&& position) {
+    const int half = p.rot >> 1, step = kRotThreads >> p.pair_shift, mine = tid >> p.pair_shift;
+    for (int t = 0; t < n; t += step * kRotAngles) {
         int32_t pos[kRotAngles];
 #pragma unroll
-        for (int k = 0; k < kRotAngles; ++k) {
-            const int tk = min(t + k * step, n - 1);
-            RotToken at{t0.b, t0.n + tk};
-            if (at.n >= p.N) at = rot_token(p, tok0 + tk);
-            pos[k] = p.pos[at.b * p.pos_sb + at.n * p.pos_sn];
-        }
+        for (int k = 0; k < kRotAngles; ++k) pos[k] = position(min(t + mine + k * step, n - 1));
         float c[kRotAngles], s[kRotAngles];
 #pragma unroll
         for (int k = 0; k < kRotAngles; ++k) {
             // the upper half as a signed number: [-1/2, 1/2) turns times 2^32
-            const int32_t part = (int32_t)(((uint64_t)(int64_t)pos[k] * frac) >> 32);
+            const int32_t part = (int32_t)(((uint64_t)(int64_t)pos[k] * pair.frac) >> 32);
             sincospif((float)part * 4.656612873077393e-10f, &s[k], &c[k]);   // 2 turns
         }
 #pragma unroll
         for (int k = 0; k < kRotAngles; ++k)
-            if (t + k * step < n)
-                cs[(t + k * step) * half + i] =
+            if (pair.i < half && t + mine + k * step < n)
+                cs[(t + mine + k * step) * half + pair.i] =
                     make_float2(c[k] * p.cs_scale, s[k] * p.cs_scale * p.sin_sign);
     }
 }
@@ -381,7 +386,12 @@ __global__ void __launch_bounds__(kRotThreads, kRotBlocksPerSm) fa_qk_rotary_fwd
     int before = input == 0 ? 0 : input == 1 ? p.H : p.H + p.H_kv;        // virtual heads
     uint4 u[kRotUnroll][2];
     load(input, lo - before, min(hi - before, input == 0 ? p.H : p.H_kv), u);
-    if (input < 2) rotary_table(cs, p, tok0, t0, tt, tid);
+    if (input < 2)
+        rotary_table(cs, p, rot_pair(p, tid), (int)min((int64_t)tt, p.tokens - tok0), tid, [&](int t) {
+            RotToken a{t0.b, t0.n + t};
+            if (a.n >= p.N) a = rot_token(p, tok0 + t);
+            return p.pos[a.b * p.pos_sb + a.n * p.pos_sn];
+        });
     __syncthreads();
 
     bool write = live, stored = live;
@@ -503,7 +513,9 @@ __global__ void __launch_bounds__(kRotThreads, kRotBlocksPerSm) fa_qk_rotary_fwd
 // kRotBwdDepth - 1 rows of g and x under way by cp.async into slots of its own
 // in shared memory, across tiles; no other thread reads them, so no barrier is
 // needed but around the angles. (With two rows in registers instead 52 us for
-// the 41 of B2 H16 N4096 d128, and 123 for 103 at B4 H32 H_kv8.)
+// 41 at B2 H16 N4096 d128, and 123 for 103 at B4 H32 H_kv8.) The next tile's
+// positions are loaded a tile ahead: with their wait in the way it took 41 us
+// for 38, and 103 for 95.
 constexpr int kRotBwdBlocks = 3 * 148;
 constexpr int kRotBwdDepth = 5;
 
@@ -562,25 +574,32 @@ __global__ void __launch_bounds__(kRotThreads, kRotBwdBlocks / 148)
     for (int j = 0; j < 4; ++j) dw0[j] = dw1[j] = f2_make(0.f, 0.f);
 
     // past a tile's last token the batch's first stands in, unused
-    auto token_at = [&](uint32_t tile, RotToken* t0) {
-        const int64_t tok0 = (int64_t)tile << p.tt_shift;
-        *t0 = rot_token(p, tok0);
-        RotToken at{t0->b, t0->n + ts};
-        if (tok0 + ts >= p.tokens) at = RotToken{0, 0};
-        else if (at.n >= p.N) at = rot_token(p, tok0 + ts);
-        return at;
+    auto token_at = [&](uint32_t tile, int t) {
+        const int64_t tok = ((int64_t)tile << p.tt_shift) + t;
+        return rot_token(p, tok < p.tokens ? tok : 0);
+    };
+    // Every warp holds its tile's positions, lane t that of token t (a tile has
+    // kSlots tokens at most), loaded while it works on the tile before.
+    static_assert(C::kSlots <= 32);
+    auto position_of = [&](uint32_t tile) {
+        const RotToken at = token_at(tile, tid & (tt - 1));
+        return p.pos[at.b * p.pos_sb + at.n * p.pos_sn];
     };
     RotCursor put{first / sd.per_tile, first % sd.per_tile};
     RotCursor get = put;
     int put_i = 0;
     const uint8_t *g_in = nullptr, *x_in = nullptr;
     auto enter = [&]() {
-        RotToken t0;
-        const RotToken at = token_at(put.tile, &t0);
+        const RotToken at = token_at(put.tile, ts);
         g_in = sd.g.ptr + (at.b * sd.g.sb + at.n * sd.g.sn) * 2;
         x_in = sd.x.ptr + (at.b * sd.x.sb + at.n * sd.x.sn) * 2;
     };
-    if (count > 0) enter();
+    const RotPair pair = rot_pair(p, tid);
+    int32_t position = 0;
+    if (count > 0) {
+        position = position_of(get.tile);
+        enter();
+    }
     auto issue = [&](int at_slot) {
         if (put_i < count) {
             const int h = min((int)put.s * h_step + h_off, sd.heads - 1);
@@ -601,14 +620,15 @@ __global__ void __launch_bounds__(kRotThreads, kRotBwdBlocks / 148)
     uint8_t* out = nullptr;
     for (int i = 0, from = 0; i < count; ++i) {
         if (fresh) {
-            RotToken t0;
-            const RotToken at = token_at(get.tile, &t0);
+            const RotToken at = token_at(get.tile, ts);
             const int64_t tok0 = (int64_t)get.tile << p.tt_shift;
             live = tok0 + ts < p.tokens;
             out = sd.out.ptr + (at.b * sd.out.sb + at.n * sd.out.sn) * 2;
             if (i > 0) __syncthreads();                      // the last tile's angles are read
-            rotary_table(cs, p, tok0, t0, tt, tid);
+            rotary_table(cs, p, pair, (int)min((int64_t)tt, p.tokens - tok0), tid,
+                         [&](int t) { return __shfl_sync(0xffffffffu, position, t); });
             __syncthreads();
+            position = position_of(get.tile + 1);
             lane_angles<kInter>(cs + ts * (p.rot >> 1), role, t);
         }
         issue(from == 0 ? kRotBwdDepth - 1 : from - 1);      // where the row before this lay
@@ -692,16 +712,22 @@ __global__ void __launch_bounds__(1024)
     __shared__ double red[32][33];
     const int j = blockIdx.x * 32 + threadIdx.x;
     const int lo = blockIdx.y ? q_blocks : 0, hi = blockIdx.y ? blocks : q_blocks;
+    constexpr int kEach = (kRotBwdBlocks + 31) / 32;         // one side's blocks over 32 rows
+    float v[kEach];                                          // loaded together
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int r = lo + (int)threadIdx.y + 32 * i;
+        v[i] = r < hi ? part[(int64_t)r * D + j] : 0.f;
+    }
     double s = 0.0;
-    for (int r = lo + (int)threadIdx.y; r < hi; r += 32) s += (double)part[(int64_t)r * D + j];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) s += (double)v[i];
     red[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
-    if (threadIdx.y == 0) {
-        double t = 0.0;
+    s = red[threadIdx.x][threadIdx.y];                       // warp y: column y
 #pragma unroll
-        for (int r = 0; r < 32; ++r) t += red[r][threadIdx.x];
-        (blockIdx.y ? dwk : dwq)[j] = (float)t;
-    }
+    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
+    if (threadIdx.x == 0) (blockIdx.y ? dwk : dwq)[blockIdx.x * 32 + threadIdx.y] = (float)s;
 }
 
 }  // namespace fa
