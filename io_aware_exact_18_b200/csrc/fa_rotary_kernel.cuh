@@ -15,8 +15,8 @@
 // takes. So a thread owns two chunks (8 elements each) of the rows of ONE
 // token, keeps their A and B in registers and walks over the heads. In the
 // half layout they are the two chunks whose elements pair up (rotary_dim is a
-// multiple of 16, so whole chunks do), or two neighbours among those that are
-// not turned; interleaved, neighbours. No element crosses lanes then, and fp32
+// multiple of 16, so whole chunks do), or two of those that are not turned;
+// interleaved, pairs stay in a chunk and any two do. No element crosses lanes then, and fp32
 // is multiplied in pairs (2 to 5 % faster than one by one). With one chunk a
 // thread, the partner's coming by shuffle and unpacked again, a chunk took 124
 // instructions where this takes 94. A row's d / 16 lanes lie in one warp, so
@@ -194,26 +194,34 @@ __device__ __forceinline__ void rotary_table(float2* cs, const RotParams& p, con
     }
 }
 
-// A lane's two chunks and their place in the rotation: whether they are
-// turned, and their first pair of eight.
+// A lane's two chunks, whether each is turned, and its first pair of the table.
+// In one instruction a row's lanes touch neighbouring chunks wherever the layout
+// leaves the choice: with a lane's two chunks side by side, each 32-byte sector
+// is asked for twice, halves at a time (B4 H32 H_kv8 N4096 d128, interleaved:
+// the backward pass, which reads past L1, takes 143 us for 95, the forward 58.7
+// for 57.4).
 struct LaneRole {
     int c0, c1;
-    bool turned;
-    int pair0;
+    bool turned0, turned1;
+    int pair0, pair1;
 };
 
-template <bool kInter>
+template <int kLanes, bool kInter>
 __device__ __forceinline__ LaneRole lane_role(int l, int rot) {
     LaneRole r;
-    const int both = rot >> 4;                               // lanes whose chunks are turned
-    r.turned = l < both;
-    r.pair0 = 8 * l;
-    if (kInter || !r.turned) {                               // the half layout's turned lanes
-        r.c0 = 2 * l;                                        // use up chunks [0, 2 both) too
-        r.c1 = 2 * l + 1;
-    } else {
+    if constexpr (kInter) {                                  // pairs stay in a chunk
         r.c0 = l;
-        r.c1 = l + both;
+        r.c1 = l + kLanes;
+        r.turned0 = r.c0 < rot >> 3;
+        r.turned1 = r.c1 < rot >> 3;
+        r.pair0 = 4 * r.c0;
+        r.pair1 = 4 * r.c1;
+    } else {                                                 // a chunk and its partner
+        const int both = rot >> 4;                           // such lanes
+        r.turned0 = r.turned1 = l < both;
+        r.c0 = r.turned0 ? l : l + both;
+        r.c1 = r.c0 + (r.turned0 ? both : kLanes - both);
+        r.pair0 = r.pair1 = 8 * l;
     }
     return r;
 }
@@ -231,16 +239,26 @@ __device__ __forceinline__ void lane_angles(const float2* cs, const LaneRole& r,
         t.a0[j] = t.a1[j] = f2_make(1.f, 1.f);
         t.b0[j] = t.b1[j] = f2_make(0.f, 0.f);
     }
-    if (!r.turned) return;
+    if constexpr (kInter) {                                  // one pair in two elements
+        if (r.turned0) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        if constexpr (kInter) {                              // one pair in two elements
-            const float2 u = cs[r.pair0 + j], v = cs[r.pair0 + 4 + j];
-            t.a0[j] = f2_make(u.x, u.x);
-            t.b0[j] = f2_make(-u.y, u.y);
-            t.a1[j] = f2_make(v.x, v.x);
-            t.b1[j] = f2_make(-v.y, v.y);
-        } else {                                             // two pairs, half of each
+            for (int j = 0; j < 4; ++j) {
+                const float2 u = cs[r.pair0 + j];
+                t.a0[j] = f2_make(u.x, u.x);
+                t.b0[j] = f2_make(-u.y, u.y);
+            }
+        }
+        if (r.turned1) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 v = cs[r.pair1 + j];
+                t.a1[j] = f2_make(v.x, v.x);
+                t.b1[j] = f2_make(-v.y, v.y);
+            }
+        }
+    } else if (r.turned0) {                                  // two pairs, half of each
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
             const float4 u = *reinterpret_cast<const float4*>(cs + r.pair0 + 2 * j);
             t.a0[j] = t.a1[j] = f2_make(u.x, u.z);
             t.b0[j] = f2_make(-u.y, -u.w);
@@ -259,15 +277,15 @@ __device__ __forceinline__ f2 turn2(f2 a, f2 x, f2 b, f2 p) {
     return f2_make(fmaf(ca.x, u.x, cb.x * v.x), fmaf(ca.y, u.y, cb.y * v.y));
 }
 
-// The partners' elements. Where part of the head is turned, lanes that are not
-// get `zero`, so that an infinity there is not multiplied by a zero coefficient.
+// The partners' elements. Where part of the head is turned, chunks that are not
+// get zeros, so that an infinity there is not multiplied by a zero coefficient.
 // (The selects are 16 instructions a row. A branch around the products instead
 // is slower here, 61.4 us for 60.5 in the normed case below: the rows of
 // a batch are then computed one after another. The backward pass, which has one
 // row at a time, gains 2 % from it.)
 template <bool kInter>
-__device__ __forceinline__ void lane_partners(const f2 (&x0)[4], const f2 (&x1)[4], bool zero,
-                                              f2 (&p0)[4], f2 (&p1)[4]) {
+__device__ __forceinline__ void lane_partners(const f2 (&x0)[4], const f2 (&x1)[4],
+                                              bool zero0, bool zero1, f2 (&p0)[4], f2 (&p1)[4]) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         if constexpr (kInter) {
@@ -278,7 +296,8 @@ __device__ __forceinline__ void lane_partners(const f2 (&x0)[4], const f2 (&x1)[
             p0[j] = x1[j];
             p1[j] = x0[j];
         }
-        if (zero) p0[j] = p1[j] = 0ull;
+        if (zero0) p0[j] = 0ull;
+        if (zero1) p1[j] = 0ull;
     }
 }
 
@@ -291,16 +310,10 @@ __device__ __forceinline__ float row_sum(float v) {
 
 enum RotStore { kDense = 0, kPageBf16 = 1, kPageE4m3 = 2 };
 
-// Eight fp32 values to a row chunk (8 codes or 8 bf16 at element c * 8).
-template <bool kE4m3>
-__device__ __forceinline__ void store_chunk(uint8_t* row, int c, const f2 (&y)[4]) {
-    if constexpr (kE4m3) {
-        const float2 a = f2_get(y[0]), b = f2_get(y[1]), d = f2_get(y[2]), e = f2_get(y[3]);
-        *reinterpret_cast<uint2*>(row + c * 8) =
-            make_uint2(pack_e4m3x4(a.x, a.y, b.x, b.y), pack_e4m3x4(d.x, d.y, e.x, e.y));
-    } else {
-        *reinterpret_cast<uint4*>(row + c * 16) = pack8(y);
-    }
+// Eight fp32 values as e4m3 codes.
+__device__ __forceinline__ uint2 codes8(const f2 (&y)[4]) {
+    const float2 a = f2_get(y[0]), b = f2_get(y[1]), d = f2_get(y[2]), e = f2_get(y[3]);
+    return make_uint2(pack_e4m3x4(a.x, a.y, b.x, b.y), pack_e4m3x4(d.x, d.y, e.x, e.y));
 }
 
 // The coefficients times the norm's weights (the partners' for b) and `mul`.
@@ -322,7 +335,7 @@ __device__ __forceinline__ void coefficients(const float2* cs, const LaneRole& r
 #pragma unroll
         for (int j = 0; j < 4; ++j) w0[j] = w1[j] = mm;
     }
-    lane_partners<kInter>(w0, w1, false, v0, v1);
+    lane_partners<kInter>(w0, w1, false, false, v0, v1);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         t.a0[j] = f2_mul(t.a0[j], w0[j]);
@@ -360,9 +373,9 @@ __global__ void __launch_bounds__(kRotThreads, kRotBlocksPerSm) fa_qk_rotary_fwd
     const int hi = (int)((int64_t)heads * (split + 1) / p.splits);
     const int slot = tid / C::kLanes;
     const int ts = slot & (tt - 1), h_off = slot >> p.tt_shift, h_step = C::kSlots >> p.tt_shift;
-    const LaneRole role = lane_role<kInter>(tid % C::kLanes, p.rot);
-    const bool pass = !role.turned;                          // some lanes where part is turned
-    const bool part = p.rot < D;
+    const LaneRole role = lane_role<C::kLanes, kInter>(tid % C::kLanes, p.rot);
+    const bool alone0 = p.rot < D && !role.turned0;          // no partners: multiplied by 1
+    const bool alone1 = kInter ? p.rot < D && !role.turned1 : alone0;
     const bool live = tok0 + ts < p.tokens;
     const RotToken t0 = rot_token(p, tok0);
     RotToken at{t0.b, t0.n + ts};
@@ -457,7 +470,7 @@ __global__ void __launch_bounds__(kRotThreads, kRotBlocksPerSm) fa_qk_rotary_fwd
                     }
                 } else {
                     f2 p0[4], p1[4];
-                    lane_partners<kInter>(x0, x1, part && pass, p0, p1);
+                    lane_partners<kInter>(x0, x1, alone0, alone1, p0, p1);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         y0[j] = f2_fma(t.a0[j], x0[j], f2_mul(t.b0[j], p0[j]));
@@ -482,15 +495,19 @@ __global__ void __launch_bounds__(kRotThreads, kRotBlocksPerSm) fa_qk_rotary_fwd
                 }
                 if (here) {
                     if (codes) {
-                        store_chunk<true>(row, role.c0, y0);
-                        store_chunk<true>(row, role.c1, y1);
-                    } else if ((kStore != kDense && input == 2) || (!kNorm && part && pass)) {
-                        // values, and what is not turned, pass through bit for bit
-                        *reinterpret_cast<uint4*>(row + role.c0 * 16) = u[i][0];
-                        *reinterpret_cast<uint4*>(row + role.c1 * 16) = u[i][1];
+                        *reinterpret_cast<uint2*>(row + role.c0 * 8) = codes8(y0);
+                        *reinterpret_cast<uint2*>(row + role.c1 * 8) = codes8(y1);
                     } else {
-                        store_chunk<false>(row, role.c0, y0);
-                        store_chunk<false>(row, role.c1, y1);
+                        // Values, and what is not turned, pass through bit for bit.
+                        uint4* o0 = reinterpret_cast<uint4*>(row + role.c0 * 16);
+                        uint4* o1 = reinterpret_cast<uint4*>(row + role.c1 * 16);
+                        if (kStore != kDense && input == 2) {
+                            *o0 = u[i][0];
+                            *o1 = u[i][1];
+                        } else {
+                            *o0 = !kNorm && alone0 ? u[i][0] : pack8(y0);
+                            *o1 = !kNorm && alone1 ? u[i][1] : pack8(y1);
+                        }
                     }
                 }
                 row += h_step * sh;
@@ -559,8 +576,9 @@ __global__ void __launch_bounds__(kRotThreads, kRotBwdBlocks / 148)
     const int tt = 1 << p.tt_shift;
     const int slot = tid / C::kLanes;
     const int ts = slot & (tt - 1), h_off = slot >> p.tt_shift, h_step = C::kSlots >> p.tt_shift;
-    const LaneRole role = lane_role<kInter>(tid % C::kLanes, p.rot);
-    const bool alone = p.rot < D && !role.turned;            // no partners: multiplied by 1
+    const LaneRole role = lane_role<C::kLanes, kInter>(tid % C::kLanes, p.rot);
+    const bool alone0 = p.rot < D && !role.turned0;          // as in the forward
+    const bool alone1 = p.rot < D && !role.turned1;
     const bool for_k = (int)blockIdx.x >= bp.q_blocks;
     const RotBwdSide& sd = bp.side[for_k ? 1 : 0];
     const int64_t blk = blockIdx.x - (for_k ? bp.q_blocks : 0);
@@ -642,14 +660,18 @@ __global__ void __launch_bounds__(kRotThreads, kRotBwdBlocks / 148)
             unpack8(ring[from][3][tid], x1);
             f2 s2 = 0ull, s3 = 0ull, d2 = 0ull, d3 = 0ull;
             f2 y0[4], y1[4];                                 // g w, then dx
-            if (!alone) {
-                f2 p0[4], p1[4];
-                lane_partners<kInter>(g0, g1, false, p0, p1);
+            f2 p0[4], p1[4];
+            lane_partners<kInter>(g0, g1, false, false, p0, p1);
+            if (!alone0) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     g0[j] = turn2<kInter>(t.a0[j], g0[j], t.b0[j], p0[j]);
-                    g1[j] = turn2<kInter>(t.a1[j], g1[j], t.b1[j], p1[j]);
+                    if (!kInter) g1[j] = turn2<kInter>(t.a1[j], g1[j], t.b1[j], p1[j]);
                 }
+            }
+            if (kInter && !alone1) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) g1[j] = turn2<kInter>(t.a1[j], g1[j], t.b1[j], p1[j]);
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
