@@ -351,12 +351,13 @@ __device__ __forceinline__ void coefficients(const float2* cs, const LaneRole& r
 // kept on the way in registers, the first batch while the angles are computed.
 // What decides the speed is the bytes on the way: batches of two, three and
 // four rows took 75, 67 and 61 us (B1 H32 H_kv8 N16384 d128 with the norm,
-// 51 us at the copy rate; the same walk that only copies the rows, 59 us). Tried, and no faster: the work shared out evenly
+// 51 us at the copy rate; the same walk that only copies the rows, 59 us).
+// Tried, and no faster: the work shared out evenly
 // over one round of blocks (62 us; 1024 tiles over 592 places are two rounds
 // for the work of 1.7), more splits (65 us with two: each computes the angles
-// again), and rows fetched by cp.async up to eight ahead (63 us; interleaved
-// pairs 85 instead of 60: the bookkeeping of single rows costs more
-// instructions than the loads on the way give back).
+// again), and rows fetched by cp.async up to eight ahead (63 us: the
+// bookkeeping of single rows costs more instructions than the loads on the way
+// give back).
 template <int D, bool kNorm, bool kInter, int kStore>
 __global__ void __launch_bounds__(kRotThreads, kRotBlocksPerSm) fa_qk_rotary_fwd(const RotParams p) {
     using C = RotCfg<D>;
@@ -522,9 +523,11 @@ __global__ void __launch_bounds__(kRotThreads, kRotBlocksPerSm) fa_qk_rotary_fwd
 //     dw_e  += g_e x_e r,        dx_e = r (g_e w_e - x_e r^2 mean(g w x)).
 // x is read again (the forward keeps nothing), both row sums are reduced in
 // the same shuffles, and dw is kept in registers over everything a thread
-// sees: its chunk is fixed. Blocks [0, q_blocks) have
-// q's rows, the others k's, kRotBwdBlocks at most in all (three an SM); dw leaves as that many partial rows, which fa_rotary_dw
-// adds in block order: no atomics.
+// sees: its chunks are fixed. Blocks [0, q_blocks) have q's rows, the others
+// k's, kRotBwdBlocks at most in all (three an SM; four, with the weights read
+// from shared memory to make room, take 40.3 us for 37.5 at B2 H16 N4096 d128
+// and the same at B4 H32 H_kv8). dw leaves as that many partial rows, which
+// fa_rotary_dw adds in a fixed order: no atomics.
 // A side's work is its token tiles times its heads, laid end to end in steps of
 // the heads that a block takes at once and shared out evenly. A thread has
 // kRotBwdDepth - 1 rows of g and x under way by cp.async into slots of its own
