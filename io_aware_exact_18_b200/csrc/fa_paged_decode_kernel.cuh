@@ -49,8 +49,13 @@
 // the matrix pipe is idle most of the time, P enters the product as two bf16
 // parts (p rounded, and the rest rounded: 2^-16), which costs 0.5 % of the
 // time and leaves O with the rounding of its result alone; O is divided by the
-// exact sum. For e4m3 P is f16 (2^-11), and O is divided by the sum of the
-// rounded probabilities. lse takes the exact sum.
+// exact sum. For e4m3 P is f16 (2^-11, a quarter of a bf16 result's own
+// rounding), and O is divided by the sum of the rounded probabilities. f16 ends
+// at 2^-24, so p is taken 2^7 larger there: a key that weighs 2^-32 of the
+// reference key still counts (at 2^-25 it did not before, and many such keys
+// were lost to O). A second f16 part takes 2 to 9 % longer (16 heads a K/V head,
+// 8 sequences of 16384 keys: 37.7 us for 34.5; the batch of 32 below 56.0 for
+// 54.3). lse takes the exact sum.
 //
 // Measured (device time, both kernels): one sequence of 131072 tokens, 8 K/V
 // heads, d 128 89 us (537 MB: 6.1 TB/s), 16 of 2048 to 8192 tokens 57.6 us
@@ -95,6 +100,9 @@ struct PdCfg {
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kMerge = kWarps * kHeads * kPitch * 4;           // in the ring's place
     static constexpr int kStat = 3 * kWarps * kHeads * 4;                 // m, l, lr
+    // log2 of a factor in every p: a score is at most 8 above the reference, so p
+    // in f16 (2^-24 to 2^16) then reaches up to 2^15
+    static constexpr float kLift = E == 1 ? 7.f : 0.f;
     static constexpr int kSmem = kRing + kStat + kWarps * kStages * 4;
     static_assert(kWarps <= pd_warps_most(D, NT), "parts of a block");
     static_assert(kMerge <= kRing, "the merge buffer reuses the ring");
@@ -500,8 +508,8 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
         uint32_t pb[C::kGroups][NT][2], pl[C::kGroups][NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-            const float m0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0];
-            const float m1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1];
+            const float m0 = (m[nt][0] == -INFINITY ? 0.f : m[nt][0]) - C::kLift;
+            const float m1 = (m[nt][1] == -INFINITY ? 0.f : m[nt][1]) - C::kLift;
 #pragma unroll
             for (int gh = 0; gh < 2 * C::kGroups; ++gh) {    // keys qr, then qr + 8, of a group
                 const int g = gh >> 1, h = gh & 1;
@@ -574,7 +582,7 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
     };
     // log2-sum-exp of exact sum `sum` with reference m: -inf for no key at all
     auto lse2 = [](float sum, float ref) {
-        return sum == 0.f ? -INFINITY : (ref == -INFINITY ? 0.f : ref) + log2f(sum);
+        return sum == 0.f ? -INFINITY : (ref == -INFINITY ? 0.f : ref) + (log2f(sum) - C::kLift);
     };
     // whole: the unit's row; otherwise this warp's part, into slot kind (0: the
     // unit ends here, 1: it goes on)

@@ -666,3 +666,49 @@ def test_calls_in_a_row_wait_for_one_another(fa):  # noqa: F811
     for u, v in zip(a[0], b[0]):
         for p, r in zip(u, v):
             assert torch.equal(p, r)
+
+
+# ---------------------------------------------------------------- e4m3 pages: bits of q and P
+def e4m3_tail(n, d):
+    """n keys and values: value 0 is zero, the others' are positive; the others'
+    keys are 0 to 4 in element 0."""
+    k = torch.zeros(n, d)
+    k[1:, 0] = (torch.arange(n - 1) % 9) * 0.5
+    v = torch.zeros(n, d)
+    v[1:] = 1 + 0.125 * ((torch.arange(n - 1)[:, None] + torch.arange(d)) % 8)
+    return k, v
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("heads", [1, 3, 12])
+@pytest.mark.parametrize("top", [20.0, 26.0, 28.0])
+@pytest.mark.parametrize("B,n", [(1, 40), (60, 5000)])
+def test_decode_e4m3_small_probabilities(fa, B, n, top, heads, d):  # noqa: F811
+    """One key outweighs each of the others by 2^16 to 2^28, and O is the others'
+    alone; one step a warp, and several. Codes, values and, but for the scale's
+    rounding (2^-24 of 28), scores (scale ln 2: log2 units) are exact. A weight is
+    off by 2^-19 (that and the exponential) and 2^-11 (f16) relative, and by 2^-32
+    of the largest (half an f16 step, 2^-24, at p taken 2^7 larger): O by that
+    times |v - O|. The sums add 2^-17 as in decode_and_check, O's rounding 2^-8."""
+    page = 16
+    k, v = e4m3_tail(n, d)
+    k[0, 0] = top
+    width = -(-n // page)
+    kc, vc = (torch.zeros(width * page, d) for _ in range(2))
+    kc[:n], vc[:n] = k, v
+    kc, vc = (c.view(width, 1, page, d).to(E4M3).to(DEV) for c in (kc, vc))
+    q = torch.zeros(B, heads, 1, d, dtype=torch.bfloat16, device=DEV)
+    q[..., 0] = 1
+    table = torch.arange(width, dtype=torch.int32, device=DEV).expand(B, width)
+    lens = torch.full((B,), n, dtype=torch.int32, device=DEV)
+    o, lse = fa.paged_decode_attention(q, kc, vc, table, lens, scale=math.log(2.0))
+    k, v = np64(k), np64(v)
+    w = np.exp2(k[:, 0] - top)
+    want = w @ v / w.sum()
+    away = np.abs(v - want)
+    tol = (2.0 ** -19 + 2.0 ** -11) * (w @ away) / w.sum() + 2.0 ** -32 * away.sum(0) / w.sum() \
+        + (2.0 ** -17 + 2.0 ** -8) * want
+    err = np.abs(np64(o)[:, :, 0] - want)
+    assert np.all(err <= tol), f"{(err / want).max()} of O"
+    want = math.log(w.sum()) + top * math.log(2.0)
+    assert np.all(np.abs(np64(lse) - want) <= 2.0 ** -16 + U * want)
