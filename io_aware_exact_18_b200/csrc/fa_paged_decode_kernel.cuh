@@ -43,7 +43,8 @@
 // reference. e4m3 keys and values are widened exactly to f16 (one conversion
 // for two) and multiplied there; q, whose bf16 range f16 lacks, is scaled by a
 // power of two per head first, which is exact but for elements 2^-31 below the
-// head's largest.
+// head's largest (its largest lies in [2^14, 2^15) then, where f16's smallest
+// step, 2^-24, is the last bit of a bf16 value 2^-31 below).
 //
 // Roundings. bf16 values want bf16 probabilities, off by up to 2^-8 each; as
 // the matrix pipe is idle most of the time, P enters the product as two bf16
@@ -384,7 +385,8 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
         for (int nt = 0; nt < NT; ++nt) {
             sc[nt][0] = sc[nt][1] = p.scale_log2;
             if constexpr (E == 1) {
-                // f16 q, scaled to a largest magnitude in [1, 2)
+                // f16 q, scaled to a largest magnitude in [2^14, 2^15): both scales
+                // stay normal numbers whatever the head's magnitude
                 float amax = 0.f;
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
@@ -395,9 +397,8 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
                 amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
                 int ex = (int)(__float_as_uint(amax) >> 23) - 127;
-                if (amax == 0.f || ex > 127) ex = 0;         // zeros; infinities stay infinite
-                ex = max(-100, min(100, ex));
-                const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+                ex = max(-112, min(127, ex));                // infinities stay infinite
+                const float down = __uint_as_float((uint32_t)(127 + 14 - ex) << 23);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
@@ -409,7 +410,7 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {                // of this thread's two columns
                     const int e2 = __shfl_sync(0xffffffffu, ex, (2 * qc + j) * 4);
-                    sc[nt][j] = p.scale_log2 * __uint_as_float((uint32_t)(127 + e2) << 23);
+                    sc[nt][j] = p.scale_log2 * __uint_as_float((uint32_t)(127 - 14 + e2) << 23);
                 }
             }
 #pragma unroll

@@ -712,3 +712,47 @@ def test_decode_e4m3_small_probabilities(fa, B, n, top, heads, d):  # noqa: F811
     assert np.all(err <= tol), f"{(err / want).max()} of O"
     want = math.log(w.sum()) + top * math.log(2.0)
     assert np.all(np.abs(np64(lse) - want) <= 2.0 ** -16 + U * want)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("below", [18, 21, 24, 30])
+def test_decode_e4m3_query_spread(fa, below, d):  # noqa: F811
+    """The scores come from elements 2^-below of the query's largest one, which
+    meets zeros: bf16 elements down to 2^-31 of the largest count in full."""
+    heads, n, page = 5, 200, 16
+    kc, vc, ks, vs = pages_of(-(-n // page), 1, page, d, 1, seed=below, ks=0.02)
+    kc = kc.float()
+    kc[..., 0] = 0
+    kc = kc.to(E4M3)
+    q = queries(1, heads, d, seed=below).float().clamp(-2, 2)
+    q = (q.abs().clamp(min=0.5) * q.sign() * 2.0 ** -below)
+    q[..., 0] = 1.5
+    table = torch.arange(kc.shape[0], dtype=torch.int32, device=DEV)[None]
+    lens = torch.tensor([n], dtype=torch.int32, device=DEV)
+    decode_and_check(fa, q.to(torch.bfloat16), kc, vc, ks, vs, table, lens,
+                     scale=2.0 ** below / math.sqrt(d))
+
+
+@pytest.mark.parametrize("mult", [2.0 ** -122, 2.0 ** -90, 2.0 ** 100, 2.0 ** 118])
+def test_decode_e4m3_query_extremes(fa, mult):  # noqa: F811
+    """Magnitudes near both ends of bf16: the power of two follows them there."""
+    kc, vc, ks, vs = pages_of(8, 1, 16, 128, 1, seed=9)
+    table = torch.arange(8, dtype=torch.int32, device=DEV)[None]
+    lens = torch.tensor([120], dtype=torch.int32, device=DEV)
+    decode_and_check(fa, queries(1, 5, 128, mult=mult), kc, vc, ks, vs, table, lens,
+                     scale=0.1 / mult)
+
+
+def test_decode_e4m3_infinite_query_element(fa):  # noqa: F811
+    """An infinite element beside large finite ones: only what meets it is not a
+    number; a head beside it is as without it."""
+    kc, vc, ks, vs = pages_of(8, 1, 16, 64, 1, seed=9)
+    q = queries(1, 3, 64)
+    table = torch.arange(8, dtype=torch.int32, device=DEV)[None]
+    lens = torch.tensor([120], dtype=torch.int32, device=DEV)
+    want = fa.paged_decode_attention(q, kc, vc, table, lens, k_descale=ks, v_descale=vs)
+    q[0, 1, 0, 5] = float("inf")
+    o, lse = fa.paged_decode_attention(q, kc, vc, table, lens, k_descale=ks, v_descale=vs)
+    for h in (0, 2):
+        assert torch.equal(o[:, h], want[0][:, h]) and torch.equal(lse[:, h], want[1][:, h])
+    assert torch.isnan(lse[0, 1]).all() and torch.isnan(o[0, 1]).all()
