@@ -756,3 +756,25 @@ def test_decode_e4m3_infinite_query_element(fa):  # noqa: F811
     for h in (0, 2):
         assert torch.equal(o[:, h], want[0][:, h]) and torch.equal(lse[:, h], want[1][:, h])
     assert torch.isnan(lse[0, 1]).all() and torch.isnan(o[0, 1]).all()
+
+
+@pytest.mark.parametrize("elem", [2, 1])
+@pytest.mark.parametrize("d,H,H_kv", [(64, 12, 12), (128, 32, 8), (128, 16, 1), (256, 40, 2)])
+def test_decode_repeats_itself(fa, d, H, H_kv, elem):  # noqa: F811
+    """The same bits every time: into other outputs, over other workspace
+    contents, after other calls."""
+    page, lens = 16, [777, 1, 0, 2000, 64, 350]
+    B, width = len(lens), -(-2000 // page)
+    kc, vc, ks, vs = pages_of(B * width, H_kv, page, d, elem, seed=d + H)
+    table = shuffled_table(B * width, B, width)
+    n = torch.tensor(lens, dtype=torch.int32, device=DEV)
+    q, other = queries(B, H, d, seed=1), queries(B, H, d, seed=2)
+    need = fa.load_library().fa_paged_decode_workspace_bytes(B, H, H_kv, d)
+    kw = dict(k_descale=ks, v_descale=vs)
+    o, lse = fa.paged_decode_attention(q, kc, vc, table, n, **kw)
+    for fill in (0, 0xFF, 0x3C):
+        ws = torch.full((need,), fill, dtype=torch.uint8, device=DEV)
+        for _ in range(3):
+            fa.paged_decode_attention(other, kc, vc, table, n.flip(0), workspace=ws, **kw)
+            o2, lse2 = fa.paged_decode_attention(q, kc, vc, table, n, workspace=ws, **kw)
+            assert torch.equal(o, o2) and torch.equal(lse, lse2)
