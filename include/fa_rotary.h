@@ -29,8 +29,9 @@
  *   - The kernels hold no bounded waits: the device status word of
  *     fa_last_device_error is neither read nor written.
  *   - d is 64, 128 or 256 (else FA_ERR_UNSUPPORTED). rotary_dim is a multiple
- *     of 16 in [0, d] (0: the norm alone, freqs may be NULL); norm_eps is
- *     finite and >= 0; rotary_scale is finite.
+ *     of 16 in [0, d] (0: the norm alone, freqs may be NULL, positions may
+ *     not: they are read all the same); norm_eps is finite and >= 0;
+ *     rotary_scale is finite.
  *   - Rows may be given any position, negative ones too.
  */
 #ifndef FA_ROTARY_H_

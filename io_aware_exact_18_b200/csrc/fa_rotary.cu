@@ -57,8 +57,8 @@ int views_check(const View* in, int n_in, const View* out, int n_out, const int*
 bool spans_apart(const fa_rotary_t& r, const int32_t* pos, int64_t sb, int64_t sn, int B, int N,
                  int d, const View* out, int n_out) {
     const ReadSpan reads[4] = {
-        r.rotary_dim > 0 ? positions_span(pos, sb, sn, B, N) : ReadSpan{nullptr, 0}, freqs_span(r),
-        weight_span(r, r.q_weight, d), weight_span(r, r.k_weight, d)};
+        positions_span(pos, sb, sn, B, N), freqs_span(r), weight_span(r, r.q_weight, d),
+        weight_span(r, r.k_weight, d)};
     for (const ReadSpan& x : reads)
         for (int o = 0; o < n_out; ++o)
             if (bytes_meet(out[o].t.ptr, view_bytes(out[o]), x.p, x.n)) return false;
@@ -89,9 +89,8 @@ int fwd(const fa_qk_rotary_t& a, void* stream) {
     if (rc == FA_OK) rc = sizes_check(a.B, a.H, a.H_kv, a.N);
     if (rc != FA_OK) return rc;
     if (a.B == 0 || a.N == 0 || a.H + a.H_kv == 0) return FA_OK;
-    if (a.rotary.rotary_dim > 0 &&
-        !positions_ok(a.positions, a.pos_stride_b, a.pos_stride_n, a.B, a.N))
-        return FA_ERR_INVALID_ARG;
+    if (!positions_ok(a.positions, a.pos_stride_b, a.pos_stride_n, a.B, a.N))
+        return FA_ERR_INVALID_ARG;       // read whatever rotary_dim is
     const View in[2] = {{a.q, a.B, a.H, a.N, a.d}, {a.k, a.B, a.H_kv, a.N, a.d}};
     const View out[2] = {{a.q_out, a.B, a.H, a.N, a.d}, {a.k_out, a.B, a.H_kv, a.N, a.d}};
     const int replaces[2] = {0, 1};
@@ -174,9 +173,8 @@ int bwd(const fa_qk_rotary_bwd_t& a, void* ws, size_t ws_bytes, void* stream) {
                    ? FA_OK
                    : FA_ERR_LAUNCH;
     }
-    if (a.rotary.rotary_dim > 0 &&
-        !positions_ok(a.positions, a.pos_stride_b, a.pos_stride_n, a.B, a.N))
-        return FA_ERR_INVALID_ARG;
+    if (!positions_ok(a.positions, a.pos_stride_b, a.pos_stride_n, a.B, a.N))
+        return FA_ERR_INVALID_ARG;       // read whatever rotary_dim is
     const View in[4] = {{a.dq_out, a.B, a.H, a.N, a.d}, {a.dk_out, a.B, a.H_kv, a.N, a.d},
                         {a.q, a.B, a.H, a.N, a.d}, {a.k, a.B, a.H_kv, a.N, a.d}};
     const View out[2] = {{a.dq, a.B, a.H, a.N, a.d}, {a.dk, a.B, a.H_kv, a.N, a.d}};

@@ -249,3 +249,33 @@ def test_oracle_gradient_by_differences(interleaved, eps):
             step[j] = 1e-6
             num = (loss(x, w + step) - loss(x, w - step)) / 2e-6
             assert abs(num - dw[j]) < 1e-6, (j, num, dw[j])
+
+
+@pytest.mark.parametrize("over", [dict(pos=0), dict(pos=P + 4 * G + 2), dict(psb=-1), dict(psn=-1),
+                                  dict(pos=P + 2 * G + 4)])
+@pytest.mark.parametrize("norm", [0, 1])
+def test_positions_are_checked_whatever_is_turned(lib, over, norm):
+    """The kernels read positions with rotary_dim 0 too: NULL, misaligned ones,
+    and ones under an output are refused there as anywhere, forward and backward."""
+    a = dict(GOOD, rot=0, freqs=0, norm=norm, **over)
+    assert lib.fa_qk_rotary(pack_fwd(a), None) == fa.FA_ERR_INVALID_ARG
+    none = {} if norm else dict(dwq=0, dwk=0)
+    assert backward(lib, rot=0, freqs=0, norm=norm, **none, **over) == fa.FA_ERR_INVALID_ARG
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the accepted calls would launch on fake pointers")
+def test_norm_alone_is_accepted(lib):
+    assert accepted(lib, rot=0, freqs=0)
+    assert backward(lib, rot=0, freqs=0) != fa.FA_ERR_INVALID_ARG
+    assert backward(lib, rot=0, freqs=0, norm=0, dwq=0, dwk=0) != fa.FA_ERR_INVALID_ARG
+
+
+def backward(lib, **over):
+    a = dict(BWD, **over)
+    qs, ks = strides(a, a["H"]), strides(a, a["H_kv"])
+    args = rotary._QK_BWD.pack(a["gq"], *qs, a["gk"], *ks, a["q"], *qs, a["k"], *ks, a["qo"], *qs,
+                               a["ko"], *ks, a["pos"], a["psb"], a["psn"], a["freqs"], a["wq"],
+                               a["wk"], a["rot"], a["inter"], a["norm"], a["w32"], a["scale"],
+                               a["eps"], a["dwq"], a["dwk"], a["B"], a["H"], a["H_kv"], a["N"],
+                               a["d"], 0)
+    return lib.fa_qk_rotary_bwd(args, a["ws"], a["ws_bytes"], None)
