@@ -53,15 +53,21 @@ int views_check(const View* in, int n_in, const View* out, int n_out, const int*
     return FA_OK;
 }
 
-// Outputs against positions, frequencies and weights.
+struct WriteSpan {
+    const void* p;
+    size_t n;
+};
+WriteSpan write_span(const View& v) { return WriteSpan{v.t.ptr, view_bytes(v)}; }
+
+// The n spans that a call writes against positions, frequencies and weights.
 bool spans_apart(const fa_rotary_t& r, const int32_t* pos, int64_t sb, int64_t sn, int B, int N,
-                 int d, const View* out, int n_out) {
+                 int d, const WriteSpan* out, int n) {
     const ReadSpan reads[4] = {
         positions_span(pos, sb, sn, B, N), freqs_span(r), weight_span(r, r.q_weight, d),
         weight_span(r, r.k_weight, d)};
     for (const ReadSpan& x : reads)
-        for (int o = 0; o < n_out; ++o)
-            if (bytes_meet(out[o].t.ptr, view_bytes(out[o]), x.p, x.n)) return false;
+        for (int o = 0; o < n; ++o)
+            if (bytes_meet(out[o].p, out[o].n, x.p, x.n)) return false;
     return true;
 }
 
@@ -96,7 +102,8 @@ int fwd(const fa_qk_rotary_t& a, void* stream) {
     const int replaces[2] = {0, 1};
     rc = views_check(in, 2, out, 2, replaces);
     if (rc != FA_OK) return rc;
-    if (!spans_apart(a.rotary, a.positions, a.pos_stride_b, a.pos_stride_n, a.B, a.N, a.d, out, 2))
+    const WriteSpan writes[2] = {write_span(out[0]), write_span(out[1])};
+    if (!spans_apart(a.rotary, a.positions, a.pos_stride_b, a.pos_stride_n, a.B, a.N, a.d, writes, 2))
         return FA_ERR_INVALID_ARG;
     int dev = 0;
     rc = device_ready(&dev);
@@ -181,14 +188,16 @@ int bwd(const fa_qk_rotary_bwd_t& a, void* ws, size_t ws_bytes, void* stream) {
     const int replaces[2] = {0, 1};
     rc = views_check(in, norm ? 4 : 2, out, 2, replaces);
     if (rc != FA_OK) return rc;
-    if (!spans_apart(a.rotary, a.positions, a.pos_stride_b, a.pos_stride_n, a.B, a.N, a.d, out, 2))
-        return FA_ERR_INVALID_ARG;
     const size_t need =
         norm ? (size_t)bwd_blocks_of(a.B, a.H, a.H_kv, a.N, a.d) * a.d * 4 : 0;
+    const size_t dw_bytes = norm ? 4 * (size_t)a.d : 0;
+    const WriteSpan writes[5] = {{ws, need}, {a.dq_weight, dw_bytes}, {a.dk_weight, dw_bytes},
+                                 write_span(out[0]), write_span(out[1])};
+    if (!spans_apart(a.rotary, a.positions, a.pos_stride_b, a.pos_stride_n, a.B, a.N, a.d, writes, 5))
+        return FA_ERR_INVALID_ARG;
     if (norm) {
         if (ws == nullptr || (addr(ws) & 15u) != 0 || ws_bytes < need) return FA_ERR_INVALID_ARG;
-        struct Buf { const void* p; size_t n; };
-        const Buf w[3] = {{ws, need}, {a.dq_weight, 4 * (size_t)a.d}, {a.dk_weight, 4 * (size_t)a.d}};
+        const WriteSpan* w = writes;
         for (int i = 0; i < 3; ++i) {
             for (const View& v : in)
                 if (bytes_meet(w[i].p, w[i].n, v.t.ptr, view_bytes(v))) return FA_ERR_INVALID_ARG;

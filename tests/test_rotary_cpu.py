@@ -279,3 +279,27 @@ def backward(lib, **over):
                                a["eps"], a["dwq"], a["dwk"], a["B"], a["H"], a["H_kv"], a["N"],
                                a["d"], 0)
     return lib.fa_qk_rotary_bwd(args, a["ws"], a["ws_bytes"], None)
+
+
+@pytest.mark.parametrize("what", ["ws", "dwq", "dwk"])
+@pytest.mark.parametrize("under", ["pos", "freqs", "wq", "wk"])
+@pytest.mark.parametrize("rot", [64, 0])
+def test_backward_refuses_to_write_over_what_it_reads(lib, what, under, rot):
+    """The workspace and the weight gradients, over the start and the last element
+    of positions, frequencies and norm weights (bf16 and fp32)."""
+    last = dict(pos=4 * 199, freqs=8 * 31, wq=2 * 127, wk=2 * 127)[under]
+    for w32 in (0, 1):
+        for off in (0, last * (2 if w32 and under[0] == "w" else 1)):
+            over = {what: (BWD[under] + off) & ~15, "rot": rot, "w32": w32}
+            if rot == 0 and under == "freqs":
+                continue                                     # not read
+            assert backward(lib, **over) == fa.FA_ERR_INVALID_ARG, (what, under, off)
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the accepted calls would launch on fake pointers")
+def test_backward_accepts_neighbours(lib):
+    """Right behind what is read, and over frequencies that rotary_dim 0 leaves unread."""
+    for what in ("ws", "dwq", "dwk"):
+        for under, size in (("pos", 4 * 200), ("freqs", 8 * 32), ("wq", 2 * 128), ("wk", 2 * 128)):
+            assert backward(lib, **{what: BWD[under] + size}) != fa.FA_ERR_INVALID_ARG, (what, under)
+        assert backward(lib, **{what: BWD["freqs"], "rot": 0}) != fa.FA_ERR_INVALID_ARG
