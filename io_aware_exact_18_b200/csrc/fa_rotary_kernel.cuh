@@ -520,7 +520,7 @@ __global__ void __launch_bounds__(kRotThreads, kRotBlocksPerSm) fa_qk_rotary_fwd
 // ---------------------------------------------------------------- backward
 // With g the output gradient turned back (the rotation's transpose, times s)
 // and r as in the forward:
-//     dw_e  += g_e x_e r,        dx_e = r (g_e w_e - x_e r^2 mean(g w x)).
+//     dw_e  += g_e n_e,   dx_e = r (g_e w_e - n_e mean(g w n)),   n = x r.
 // x is read again (the forward keeps nothing), both row sums are reduced in
 // the same shuffles, and dw is kept in registers over everything a thread
 // sees: its chunks are fixed. Blocks [0, q_blocks) have q's rows, the others
@@ -692,15 +692,18 @@ __global__ void __launch_bounds__(kRotThreads, kRotBwdBlocks / 148)
                 dot += __shfl_xor_sync(0xffffffffu, dot, off);
             }
             const float r = rsqrtf(fmaf(ss, 1.f / D, p.eps));
-            const float k = -r * r * r * dot * (1.f / D);
+            // mean(g w n), then r: each of the size of what it stands for, where r^3
+            // would leave fp32's normal numbers for rows of rms 2^42 or 2^-43
+            const float k = -(r * dot * (1.f / D)) * r;
             if (live && h < sd.heads) {
                 const f2 rr = f2_make(r, r), kk = f2_make(k, k);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    dw0[j] = f2_fma(f2_mul(g0[j], rr), x0[j], dw0[j]);
-                    dw1[j] = f2_fma(f2_mul(g1[j], rr), x1[j], dw1[j]);
-                    y0[j] = f2_fma(y0[j], rr, f2_mul(x0[j], kk));
-                    y1[j] = f2_fma(y1[j], rr, f2_mul(x1[j], kk));
+                    const f2 n0 = f2_mul(x0[j], rr), n1 = f2_mul(x1[j], rr);
+                    dw0[j] = f2_fma(g0[j], n0, dw0[j]);
+                    dw1[j] = f2_fma(g1[j], n1, dw1[j]);
+                    y0[j] = f2_fma(y0[j], rr, f2_mul(n0, kk));
+                    y1[j] = f2_fma(y1[j], rr, f2_mul(n1, kk));
                 }
                 uint8_t* row = out + h * sd.out.sh * 2;
                 *reinterpret_cast<uint4*>(row + role.c0 * 16) = pack8(y0);

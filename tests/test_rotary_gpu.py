@@ -368,3 +368,34 @@ def test_gradient_by_differences(fa, norm):
             up = (g * orot.forward(x + h * v, p64, f64, False, 1.0, norm)).sum()
             down = (g * orot.forward(x - h * v, p64, f64, False, 1.0, norm)).sum()
             assert abs((up - down) / (2 * h) - (dx * v).sum()) <= 2.0 ** -8 * np.abs(dx * v).sum()
+
+
+@pytest.mark.parametrize("d,rot", [(64, 64), (128, 48), (256, 256)])
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("power,eps", [(50, 1e-6), (30, 1e-6), (-50, 0.0), (-44, 1e-30)])
+def test_backward_of_large_and_small_rows(fa, power, eps, inter, d, rot):
+    """Rows of rms 2^50 and 2^-50, where r^3 leaves fp32 while r, the row sums and
+    the gradients are ordinary numbers; gradients along x, so that the mean's term
+    counts. Each product is rounded as in test_backward: its bound."""
+    B, H, H_kv, N = 2, 3, 1, 11
+    q, k = make(B, H, H_kv, N, d, seed=d)
+    gq, gk = make(B, H, H_kv, N, d, seed=d + 1)
+    gq, gk = (0.5 * gq + q).to(torch.bfloat16), (0.5 * gk + k).to(torch.bfloat16)
+    q, k = q * 2.0 ** power, k * 2.0 ** power
+    pos = torch.arange(N, dtype=torch.int32, device=DEV).expand(B, N)
+    freqs = fa.rotary_frequencies(rot)
+    wq, wk = weights(d, True)
+    got = fa.qk_rotary_bwd(gq, gk, q, k, pos, freqs, interleaved=inter, norm_eps=eps, q_weight=wq,
+                           k_weight=wk)
+    for x, dy, w, dx, dw, name in ((q, gq, wq, got[0], got[2], "q"),
+                                   (k, gk, wk, got[1], got[3], "k")):
+        x64, dy64, w64 = np64(x), np64(dy), np64(w)
+        eps64 = float(np.float32(eps))
+        rx, rw = orot.backward(dy64, x64, np64(pos), np64(freqs), inter, 1.0, eps64, w64)
+        g = partner_sum(dy64, len(freqs), inter)
+        r = 1 / np.sqrt((x64 * x64).mean(-1, keepdims=True) + eps64)
+        n = np.abs(x64 * r)
+        gw = g * np.abs(w64)
+        tol = 2.0 ** -8 * np.abs(rx) + 64 * U * r * (gw + n * (gw * n).mean(-1, keepdims=True))
+        assert np.all(np.abs(np64(dx) - rx) <= tol + TINY), f"d{name}"
+        assert np.all(np.abs(np64(dw) - rw) <= 256 * U * (g * n).reshape(-1, d).sum(0)), name
