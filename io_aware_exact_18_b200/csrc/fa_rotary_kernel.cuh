@@ -335,7 +335,8 @@ __device__ __forceinline__ void coefficients(const float2* cs, const LaneRole& r
 #pragma unroll
         for (int j = 0; j < 4; ++j) w0[j] = w1[j] = mm;
     }
-    lane_partners<kInter>(w0, w1, false, false, v0, v1);
+    // (where nothing is turned b is zero, and stays so beside an infinite weight)
+    lane_partners<kInter>(w0, w1, kNorm && !role.turned0, kNorm && !role.turned1, v0, v1);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         t.a0[j] = f2_mul(t.a0[j], w0[j]);

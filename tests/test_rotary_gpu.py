@@ -399,3 +399,25 @@ def test_backward_of_large_and_small_rows(fa, power, eps, inter, d, rot):
         tol = 2.0 ** -8 * np.abs(rx) + 64 * U * r * (gw + n * (gw * n).mean(-1, keepdims=True))
         assert np.all(np.abs(np64(dx) - rx) <= tol + TINY), f"d{name}"
         assert np.all(np.abs(np64(dw) - rw) <= 256 * U * (g * n).reshape(-1, d).sum(0)), name
+
+
+@pytest.mark.parametrize("inter", [False, True])
+def test_infinite_weight_stays_in_its_pair(fa, inter):
+    """An infinite weight of one element: those that are not turned, and the other
+    pairs, do not see it."""
+    q, k = make(1, 2, 2, 5, 64, seed=50)
+    pos = torch.arange(1, 6, dtype=torch.int32, device=DEV)
+    freqs = fa.rotary_frequencies(32)
+    w = torch.ones(64, device=DEV)
+    want, _ = fa.qk_rotary(q, k, pos, freqs, interleaved=inter, norm_eps=1e-6, q_weight=w)
+    for at in (40, 63, 3):
+        u = w.clone()
+        u[at] = float("inf")
+        got, _ = fa.qk_rotary(q, k, pos, freqs, interleaved=inter, norm_eps=1e-6, q_weight=u)
+        here = [at] if at >= 32 else [2, 3] if inter else [3, 19]
+        bad = ~torch.isfinite(got)
+        assert bad[..., here].all()
+        bad[..., here] = False
+        assert not bad.any()
+        rest = [i for i in range(64) if i not in here]
+        assert torch.equal(got[..., rest], want[..., rest])
