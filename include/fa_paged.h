@@ -67,7 +67,8 @@ typedef struct {
  * Writes new tokens into the cache: k normed and turned as in fa_qk_rotary,
  * then stored (bf16 or e4m3, rounded once, e4m3 saturating at 448) at its
  * sequence's position, v stored as it is, and q normed and turned into q_out,
- * in one pass. Token (b, n) goes to key positions[b][n] of table row seq[b].
+ * in one pass. e4m3 descales must have finite reciprocals (above 2^-128).
+ * Token (b, n) goes to key positions[b][n] of table row seq[b].
  * A token with a negative position is padding: nothing of it is written, in
  * the cache or q_out. One whose sequence, page slot or page does not exist is
  * dropped from the cache (its q_out row is written). Two tokens of one call

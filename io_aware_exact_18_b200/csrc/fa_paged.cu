@@ -91,6 +91,11 @@ int append(const fa_paged_append_t& a, void* stream) {
     if (a.B < 0 || a.H < 0 || a.N < 0 || (int64_t)a.B * a.N > INT32_MAX || a.H > 65536 ||
         (double)a.B * a.N * ((double)a.H + 2.0 * c.H_kv) > INT32_MAX)   // rows in 31 bits
         return FA_ERR_INVALID_ARG;
+    // Codes are x / descale; the product with the rounded reciprocal is off by
+    // 2^-23 of it, far below the 2^-4 of the e4m3 rounding that follows. A
+    // reciprocal that is infinite would make NaN of zeros.
+    const float k_inv = 1.f / c.k_descale, v_inv = 1.f / c.v_descale;
+    if (!std::isfinite(k_inv) || !std::isfinite(v_inv)) return FA_ERR_INVALID_ARG;
     if ((a.q.ptr == nullptr) != (a.q_out.ptr == nullptr)) return FA_ERR_INVALID_ARG;
     const int H = a.q.ptr == nullptr ? 0 : a.H;
     if (a.B == 0 || a.N == 0 || H + c.H_kv == 0) return FA_OK;
@@ -140,10 +145,8 @@ int append(const fa_paged_append_t& a, void* stream) {
     p.width = a.table.pages_per_seq;
     p.num_pages = c.num_pages;
     p.page_size = c.page_size;
-    // Codes are x / descale; the product with the rounded reciprocal is off by
-    // 2^-23 of it, far below the 2^-4 of the e4m3 rounding that follows.
-    p.k_inv = 1.f / c.k_descale;
-    p.v_inv = 1.f / c.v_descale;
+    p.k_inv = k_inv;
+    p.v_inv = v_inv;
     const bool norm = a.rotary.norm != 0, inter = a.rotary.interleaved != 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return c.d == 64    ? launch_append<64>(p, c.elem, norm, inter, s)

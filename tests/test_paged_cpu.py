@@ -203,3 +203,19 @@ def test_wrappers_refuse():
         fa.paged_decode_attention(x, kc.float(), kc.float(), t, t[0, :1])
     with pytest.raises(ValueError):
         fa.copy_pages(kc, kc.clone(), t[0], t[0])
+
+
+@pytest.mark.parametrize("which", ["ks", "vs"])
+@pytest.mark.parametrize("descale", [2.0 ** -149, 2.0 ** -130, 2.0 ** -128])
+def test_append_refuses_descales_without_a_reciprocal(lib, which, descale):
+    """Codes are products with 1 / descale: infinite below 2^-128, and zeros would
+    be stored as NaN."""
+    assert append(lib, elem=1, **{which: descale}) == fa.FA_ERR_INVALID_ARG
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the accepted calls would launch on fake pointers")
+def test_small_descales_are_accepted(lib):
+    """Append from the first descale on whose reciprocal is finite; reading any."""
+    assert append(lib, elem=1, ks=2.0 ** -127, vs=2.0 ** -127) != fa.FA_ERR_INVALID_ARG
+    assert append(lib, elem=1, ks=2.0 ** 127, vs=1e38) != fa.FA_ERR_INVALID_ARG
+    assert decode(lib, elem=1, ks=2.0 ** -140, vs=2.0 ** -140) != fa.FA_ERR_INVALID_ARG
