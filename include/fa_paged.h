@@ -31,7 +31,8 @@ extern "C" {
  * h * stride_head + t * stride_token + j elements from k (and from v): both
  * [pages, H_kv, page_size, d] and [pages, page_size, H_kv, d] orders fit.
  * Pointers are 16-byte aligned and strides multiples of 16 bytes, > 0 where
- * the extent is above 1. Distinct rows must not overlap. page_size is any
+ * the extent is above 1. Distinct rows must not overlap; K and V may lie in one
+ * buffer, and share no element where a call writes them. page_size is any
  * number from 1 to 65536, d is 64, 128 or 256.
  * elem 2: bf16. elem 1: e4m3 codes that stand for descale * code
  * (k_descale, v_descale finite and > 0; both must be 1 for bf16).

@@ -13,9 +13,23 @@
 namespace fa {
 namespace {
 
+// Whether two row sets of one layout, `delta` elements apart, share one: rows of
+// `row` elements at sums of i_a s_a, 0 <= i_a < n_a, the strides ascending and
+// each stepping over the whole extent of the axes below. On each axis from the
+// widest only the two multiples around delta can bring the rest within reach.
+bool rows_meet(int64_t delta, const int64_t* s, const int64_t* n, int axes, int64_t row) {
+    if (axes == 0) return delta < row && -delta < row;
+    const int64_t st = s[axes - 1], most = n[axes - 1] - 1;
+    if (most == 0) return rows_meet(delta, s, n, axes - 1, row);
+    const int64_t below = delta / st - (delta % st < 0 ? 1 : 0);         // floor
+    for (int64_t i = below; i <= below + 1; ++i)
+        if (i >= -most && i <= most && rows_meet(delta - i * st, s, n, axes - 1, row)) return true;
+    return false;
+}
+
 // The cache's own arguments; *bytes: from its first to past its last byte,
-// the same for K and V.
-int cache_check(const fa_paged_cache_t& c, size_t* bytes) {
+// the same for K and V. A call that writes it needs K and V apart.
+int cache_check(const fa_paged_cache_t& c, bool writes, size_t* bytes) {
     if (c.d != 64 && c.d != 128 && c.d != 256) return FA_ERR_UNSUPPORTED;
     if (c.elem != 1 && c.elem != 2) return FA_ERR_UNSUPPORTED;
     if (c.num_pages < 0 || c.page_size < 1 || c.page_size > 65536 || c.H_kv < 0 || c.H_kv > 65536)
@@ -47,7 +61,10 @@ int cache_check(const fa_paged_cache_t& c, size_t* bytes) {
         extent += s[i] * (n[i] - 1);
     }
     *bytes = (size_t)extent * c.elem;
-    if (addr(c.k) == addr(c.v)) return FA_ERR_INVALID_ARG;
+    const int64_t apart = (int64_t)(addr(c.v) - addr(c.k)) / c.elem;
+    if (apart == 0 || (writes && bytes_meet(c.k, *bytes, c.v, *bytes) &&
+                       rows_meet(apart, s, n, 3, c.d)))
+        return FA_ERR_INVALID_ARG;
     return FA_OK;
 }
 
@@ -84,7 +101,7 @@ int launch_append(RotParams p, int elem, bool norm, bool inter, cudaStream_t s) 
 int append(const fa_paged_append_t& a, void* stream) {
     const fa_paged_cache_t& c = a.cache;
     size_t cbytes = 0;
-    int rc = cache_check(c, &cbytes);
+    int rc = cache_check(c, true, &cbytes);
     if (rc == FA_OK) rc = rotary_check(a.rotary, c.d);
     if (rc == FA_OK) rc = table_check(a.table);
     if (rc != FA_OK) return rc;
@@ -217,7 +234,7 @@ int launch_decode_d(const PdParams& p, int elem, int nt, cudaStream_t s) {
 int decode(const fa_paged_decode_t& a, void* ws, size_t ws_bytes, void* stream) {
     const fa_paged_cache_t& c = a.cache;
     size_t cbytes = 0;
-    int rc = cache_check(c, &cbytes);
+    int rc = cache_check(c, false, &cbytes);
     if (rc == FA_OK) rc = table_check(a.table);
     if (rc != FA_OK) return rc;
     if (a.B < 0 || a.H < 0 || (int64_t)a.B * a.H > INT32_MAX / 64) return FA_ERR_INVALID_ARG;
@@ -295,7 +312,7 @@ int decode(const fa_paged_decode_t& a, void* ws, size_t ws_bytes, void* stream) 
 // ------------------------------------------------------------------ copies
 int copy(const fa_paged_cache_t& c, const int32_t* src, const int32_t* dst, int n, void* stream) {
     size_t cbytes = 0;
-    int rc = cache_check(c, &cbytes);
+    int rc = cache_check(c, true, &cbytes);
     if (rc != FA_OK) return rc;
     if (n < 0 || n > INT32_MAX / 128) return FA_ERR_INVALID_ARG;
     if (n == 0 || cbytes == 0) return FA_OK;

@@ -219,3 +219,54 @@ def test_small_descales_are_accepted(lib):
     assert append(lib, elem=1, ks=2.0 ** -127, vs=2.0 ** -127) != fa.FA_ERR_INVALID_ARG
     assert append(lib, elem=1, ks=2.0 ** 127, vs=1e38) != fa.FA_ERR_INVALID_ARG
     assert decode(lib, elem=1, ks=2.0 ** -140, vs=2.0 ** -140) != fa.FA_ERR_INVALID_ARG
+
+
+def kv_layouts():
+    """(cache fields, whether K and V share an element) for V at many offsets from K
+    in buffers that hold both, by counting the elements themselves."""
+    H, page, d = 2, 4, 64
+    cases = []
+    for pages, sp, sh, st in ((3, 2 * H * page * d, page * d, d),          # [pages, 2, H, page, d]
+                              (3, 2 * H * page * d, 2 * page * d, d),      # [pages, H, 2, page, d]
+                              (3, 2 * H * page * d, 2 * d, 2 * H * d),     # [pages, page, H, 2, d]
+                              (3, 2 * H * page * d, d, 2 * H * d),         # [pages, page, 2, H, d]
+                              (3, H * page * d, page * d, d),              # dense
+                              (1, 0, page * d + 32, d)):                   # one page, padded heads
+        rows = {p * sp + h * sh + t * st for p in range(pages) for h in range(H) for t in range(page)}
+        taken = {r + j for r in rows for j in range(0, d, 8)}
+        for off in range(-2 * max(taken), 2 * max(taken), 8 * 4):
+            shared = any(r + off + j in taken for r in rows for j in range(0, d, 8))
+            cases.append((dict(vc=P + (1 << 24) + 2 * off, kc=P + (1 << 24), sp=sp, sh=sh, st=st,
+                               pages=pages, page=page, H_kv=H, d=d), shared))
+    return cases
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the accepted calls would launch on fake pointers")
+def test_keys_and_values_that_share_elements_are_refused(lib):
+    """K and V may lie in one buffer as long as no element is both."""
+    a = dict(CACHE, src=P + 4 * G, dst=P + 5 * G)
+    some = {True: 0, False: 0}
+    for over, shared in kv_layouts():
+        a.update(over)
+        st = lib.fa_copy_pages(paged._COPY.pack(*cache_fields(a)), a["src"], a["dst"], 3, None)
+        assert (st == fa.FA_ERR_INVALID_ARG) == shared, over
+        some[shared] += 1
+    assert min(some.values()) > 100
+
+
+@pytest.mark.parametrize("over", [dict(vc=P + 256), dict(vc=P + 2 * 16 * 128 * 2),
+                                  dict(vc=P - 99 * 2 * 16 * 128 * 2),
+                                  dict(sp=4 * 16 * 128, vc=P + 2 * 16 * 128 * 2 - 256)])
+def test_overlapping_caches_are_refused(lib, over):
+    """V a row, a page or 99 pages of K away, or a row into its half of a buffer."""
+    assert append(lib, **over) == fa.FA_ERR_INVALID_ARG
+    a = dict(CACHE, **over)
+    assert lib.fa_copy_pages(paged._COPY.pack(*cache_fields(a)), P + 4 * G, P + 5 * G, 3,
+                             None) == fa.FA_ERR_INVALID_ARG
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="the accepted calls would launch on fake pointers")
+def test_reading_overlapping_caches_is_accepted(lib):
+    """Values that are part of the keys' rows, or a page away, are only read."""
+    assert decode(lib, vc=P + 2 * 16 * 128 * 2) != fa.FA_ERR_INVALID_ARG
+    assert decode(lib, st=192, sh=16 * 192, sp=2 * 16 * 192, vc=P + 128) != fa.FA_ERR_INVALID_ARG
