@@ -12,7 +12,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libfa.so")
-SOURCES = [os.path.join(CSRC, f) for f in ("fa_api.cu", "fa_rotary.cu", "fa_paged.cu")]
+SOURCES = [os.path.join(CSRC, f)
+           for f in ("fa_api.cu", "fa_device.cu", "fa_rotary.cu", "fa_paged.cu")]
 INCLUDE = os.path.join(ROOT, "include")
 HEADERS = [os.path.join(d, f) for d in (CSRC, INCLUDE) for f in os.listdir(d)
            if f.endswith((".cuh", ".h"))]

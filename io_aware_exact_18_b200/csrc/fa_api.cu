@@ -15,7 +15,6 @@
 #include "fa_combine_kernel.cuh"
 #include "fa_decode_kernel.cuh"
 #include "fa_fwd_kernel.cuh"
-#include "fa_host.h"
 
 namespace fa {
 
@@ -585,12 +584,6 @@ FwdCall square_call(const void* q, const void* k, const void* v, void* o, float*
 }
 
 }  // namespace
-
-int device_ready(int* dev_out) {
-    uint32_t* err = nullptr;
-    return prepare_device(dev_out, &err);
-}
-
 }  // namespace fa
 
 #define FA_EXPORT __attribute__((visibility("default")))

@@ -8,9 +8,8 @@
 
 namespace fa {
 
-// Capability check and set-up of the current device (once per device): FA_OK
-// and its index, or the status to return.
-int device_ready(int* dev_out);
+// Capability check of the current device: FA_OK, or the status to return.
+int device_ready();
 
 // ---------------------------------------------------------------- views
 inline uintptr_t addr(const void* p) { return reinterpret_cast<uintptr_t>(p); }

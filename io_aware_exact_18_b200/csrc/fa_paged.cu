@@ -2,7 +2,6 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
-#include <mutex>
 
 #include "fa_host.h"
 #include "fa_page_copy_kernel.cuh"
@@ -141,8 +140,7 @@ int append(const fa_paged_append_t& a, void* stream) {
         if (meets_cache(c, cbytes, r.p, r.n) ||
             (H > 0 && bytes_meet(a.q_out.ptr, view_bytes(qo), r.p, r.n)))
             return FA_ERR_INVALID_ARG;
-    int dev = 0;
-    rc = device_ready(&dev);
+    rc = device_ready();
     if (rc != FA_OK) return rc;
     RotParams p{};
     rot_fill(&p, a.rotary, a.positions, a.pos_stride_b, a.pos_stride_n, a.B, H, c.H_kv, a.N);
@@ -264,8 +262,7 @@ int decode(const fa_paged_decode_t& a, void* ws, size_t ws_bytes, void* stream) 
         for (int j = 0; j < i; ++j)
             if (bytes_meet(outs[i].p, outs[i].n, outs[j].p, outs[j].n)) return FA_ERR_INVALID_ARG;
     }
-    int dev = 0;
-    rc = device_ready(&dev);
+    rc = device_ready();
     if (rc != FA_OK) return rc;
     PdParams p{};
     p.q = static_cast<const __nv_bfloat16*>(a.q);
@@ -345,8 +342,7 @@ int copy(const fa_paged_cache_t& c, const int32_t* src, const int32_t* dst, int 
                            (c.H_kv == 1 || p.head == row * c.page_size);
     const bool tokens_out = (c.H_kv == 1 || p.head == row) &&
                             (c.page_size == 1 || p.token == row * c.H_kv);
-    int dev = 0;
-    rc = device_ready(&dev);
+    rc = device_ready();
     if (rc != FA_OK) return rc;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const dim3 grid((unsigned)blocks, 2);

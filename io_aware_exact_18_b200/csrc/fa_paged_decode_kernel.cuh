@@ -72,6 +72,7 @@
 #include <cuda_fp16.h>
 #include <cstdint>
 
+#include "cp_async.cuh"
 #include "sm100_ptx.cuh"
 
 namespace fa {

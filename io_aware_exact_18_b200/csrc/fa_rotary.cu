@@ -105,8 +105,7 @@ int fwd(const fa_qk_rotary_t& a, void* stream) {
     const WriteSpan writes[2] = {write_span(out[0]), write_span(out[1])};
     if (!spans_apart(a.rotary, a.positions, a.pos_stride_b, a.pos_stride_n, a.B, a.N, a.d, writes, 2))
         return FA_ERR_INVALID_ARG;
-    int dev = 0;
-    rc = device_ready(&dev);
+    rc = device_ready();
     if (rc != FA_OK) return rc;
     RotParams p{};
     p.q = rot_rows(a.q);
@@ -171,9 +170,8 @@ int bwd(const fa_qk_rotary_bwd_t& a, void* ws, size_t ws_bytes, void* stream) {
     const bool empty = a.B == 0 || a.N == 0 || a.H + a.H_kv == 0;
     if (empty && !norm) return FA_OK;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    int dev = 0;
     if (empty) {                      // no rows: the weights' gradients are zero
-        rc = device_ready(&dev);
+        rc = device_ready();
         if (rc != FA_OK) return rc;
         return cudaMemsetAsync(a.dq_weight, 0, 4 * a.d, s) == cudaSuccess &&
                        cudaMemsetAsync(a.dk_weight, 0, 4 * a.d, s) == cudaSuccess
@@ -206,7 +204,7 @@ int bwd(const fa_qk_rotary_bwd_t& a, void* ws, size_t ws_bytes, void* stream) {
             if (i > 0 && bytes_meet(ws, need, w[i].p, w[i].n)) return FA_ERR_INVALID_ARG;
         }
     }
-    rc = device_ready(&dev);
+    rc = device_ready();
     if (rc != FA_OK) return rc;
     RotParams p{};
     rot_fill(&p, a.rotary, a.positions, a.pos_stride_b, a.pos_stride_n, a.B, a.H, a.H_kv, a.N);

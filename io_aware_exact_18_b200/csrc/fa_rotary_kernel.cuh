@@ -34,6 +34,7 @@
 #include <cuda_bf16.h>
 #include <cstdint>
 
+#include "cp_async.cuh"
 #include "sm100_ptx.cuh"
 
 namespace fa {

@@ -189,28 +189,6 @@ __device__ __forceinline__ int clc_decode(const void* resp) {
     return ok ? (int)x : -1;
 }
 
-// 16-byte asynchronous copies global -> shared of the issuing thread: `in`
-// false writes zeros and reads nothing. Completed group by group. The second
-// form takes an L2 cache policy (createpolicy result).
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst),
-                 "l"(src), "r"(in ? 16 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool in,
-                                           uint64_t policy) {
-    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst),
-                 "l"(src), "r"(in ? 16 : 0), "l"(policy)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-    asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Programmatic dependent launch: let the grid queued after this one on the
 // stream (launched with the programmatic-serialization attribute) start once
 // every CTA of this grid has executed this or exited...

@@ -156,3 +156,10 @@ def test_decode_kernel_name_follows_the_dispatch_rule():
     assert bench.decode_kernel_name(wide, 4).startswith("fa_fwd_sm100<128,1,general>")
     d64 = workloads.DecodeWorkload("d64", 1, 32, 8, 1, 4096, 64)
     assert bench.decode_kernel_name(d64, 1) == "fa_fwd_sm100<64,1,general>"
+
+
+def test_recorded_traffic_is_of_the_present_sources():
+    """The headline workload's DRAM bytes were recorded on the kernel as it is:
+    bench.py reports them only then."""
+    got = bench.recorded_traffic(workloads.get(5).name)
+    assert got is not None and got["read"] > 0 and got["write"] > 0
