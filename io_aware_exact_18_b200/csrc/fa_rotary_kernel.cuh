@@ -500,17 +500,17 @@ __global__ void __launch_bounds__(kRotThreads, kRotBlocksPerSm) fa_qk_rotary_fwd
                     if (codes) {
                         *reinterpret_cast<uint2*>(row + role.c0 * 8) = codes8(y0);
                         *reinterpret_cast<uint2*>(row + role.c1 * 8) = codes8(y1);
+                    // Values, and what is not turned, pass through bit for bit. (One
+                    // chain of branches: with the values' inside the other's, a prompt
+                    // of 8192 into bf16 pages, normed, takes 38.5 us for 37.8.)
+                    } else if (kStore != kDense && input == 2) {
+                        *reinterpret_cast<uint4*>(row + role.c0 * 16) = u[i][0];
+                        *reinterpret_cast<uint4*>(row + role.c1 * 16) = u[i][1];
                     } else {
-                        // Values, and what is not turned, pass through bit for bit.
-                        uint4* o0 = reinterpret_cast<uint4*>(row + role.c0 * 16);
-                        uint4* o1 = reinterpret_cast<uint4*>(row + role.c1 * 16);
-                        if (kStore != kDense && input == 2) {
-                            *o0 = u[i][0];
-                            *o1 = u[i][1];
-                        } else {
-                            *o0 = !kNorm && alone0 ? u[i][0] : pack8(y0);
-                            *o1 = !kNorm && alone1 ? u[i][1] : pack8(y1);
-                        }
+                        *reinterpret_cast<uint4*>(row + role.c0 * 16) =
+                            !kNorm && alone0 ? u[i][0] : pack8(y0);
+                        *reinterpret_cast<uint4*>(row + role.c1 * 16) =
+                            !kNorm && alone1 ? u[i][1] : pack8(y1);
                     }
                 }
                 row += h_step * sh;
