@@ -778,3 +778,57 @@ def test_decode_repeats_itself(fa, d, H, H_kv, elem):  # noqa: F811
             fa.paged_decode_attention(other, kc, vc, table, n.flip(0), workspace=ws, **kw)
             o2, lse2 = fa.paged_decode_attention(q, kc, vc, table, n, workspace=ws, **kw)
             assert torch.equal(o, o2) and torch.equal(lse, lse2)
+
+
+def test_captured_forks_joins_and_copies(fa):  # noqa: F811
+    """One captured step whose calls follow two branches at once, a copy and a fill:
+    replayed on changing inputs it gives the eager step's bits. A second graph
+    holds the same step over the same workspace."""
+    B, H, H_kv, d, page = 3, 8, 2, 128, 16
+    kc, vc, _, _ = pages_of(100, H_kv, page, d, 2, seed=7)
+    table = shuffled_table(100, B, 30)
+    freqs = fa.rotary_frequencies(128)
+    x = torch.randn(B, H + 2 * H_kv, 1, d, device=DEV).to(torch.bfloat16)
+    n = torch.tensor([470, 3, 100], dtype=torch.int32, device=DEV)
+    held, left = torch.zeros_like(n), torch.zeros_like(n)
+    need = fa.load_library().fa_paged_decode_workspace_bytes(B, H, H_kv, d)
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    side = torch.cuda.Stream()
+
+    def step():
+        main = torch.cuda.current_stream()
+        left.fill_(0)
+        held.copy_(n)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            fa.paged_append(x[:, H:H + H_kv], x[:, H + H_kv:], kc, vc, table, held[:, None],
+                            freqs=freqs, norm_eps=1e-6)
+        q, k = fa.qk_rotary(x[:, :H], x[:, H:H + H_kv], held[:, None], freqs, norm_eps=1e-6)
+        main.wait_stream(side)                               # both are read next
+        left.add_(held).add_(1)
+        o, lse = fa.paged_decode_attention(q, kc, vc, table, left, workspace=ws)
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            dq, dk, dw, _ = fa.qk_rotary_bwd(o, k, x[:, :H], x[:, H:H + H_kv], held[:, None], freqs,
+                                             norm_eps=1e-6)
+        o2, lse2 = fa.paged_decode_attention(q, kc, vc, table, held, workspace=ws)
+        main.wait_stream(side)
+        return o, lse, dq, dk, dw, o2, lse2
+
+    step()
+    torch.cuda.synchronize()
+    graphs, kept = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            kept.append(step())
+        graphs.append(g)
+    for i in range(6):
+        x.copy_(torch.randn(B, H + 2 * H_kv, 1, d, device=DEV).to(torch.bfloat16))
+        graphs[i % 2].replay()
+        got = [t.clone() for t in kept[i % 2]]
+        torch.cuda.synchronize()
+        for a, b in zip(got, step()):
+            assert torch.equal(a, b)
+        torch.cuda.synchronize()
+        n.add_(1)
