@@ -98,7 +98,10 @@ typedef struct {
  * with no visible key gets O = 0 and lse = -inf. The tiles of all sequences
  * are shared out evenly over the SMs, whatever the lengths; parts of a
  * sequence are joined by a second kernel by their log-sum-exp. Slots that are
- * not visible are never used in arithmetic: they may hold NaN.
+ * not visible are never used in arithmetic: they may hold NaN. NaN and
+ * infinities in visible keys, values or queries reach what they enter and
+ * nothing else (the rows that read the key or hold the query, the value's
+ * element of those rows); an infinity may give NaN there.
  * workspace: device memory owned by the caller, 16-byte aligned, at least
  * fa_paged_decode_workspace_bytes(B, H, H_kv, d) bytes (whatever the
  * lengths), overlapping nothing else, with no initialisation; two calls in

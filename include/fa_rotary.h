@@ -12,8 +12,10 @@
  * with r = rotary_dim <= d, f_i = freqs[i] and s = rotary_scale. Pair i is
  * (y_i, y_{i + r/2}), or (y_{2i}, y_{2i+1}) with interleaved = 1; elements
  * r .. d-1 are not turned (and not scaled by s). Arithmetic is fp32, rounded
- * once to bf16; the angle is a product in 64-bit fixed-point fractions of a
- * turn, so far positions lose nothing. Frequencies are finite.
+ * once to bf16 (mean x^2 too: the norm wants rows of an rms below 2^59, and above
+ * 2^-59 where eps does not outweigh it). The angle is formed in 64-bit
+ * fixed-point fractions of a turn from f_i / 2 pi in fp64: for frequencies up to 1
+ * it is off by 2^-24 turns at most at any 32-bit position. Frequencies are finite.
  *
  * Conventions are those of fa.h (device pointers owned by the caller, status
  * codes, errors reported before any CUDA call, asynchronous calls,

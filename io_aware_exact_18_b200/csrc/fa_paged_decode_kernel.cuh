@@ -28,10 +28,12 @@
 // by shuffle: any page size and page order costs the same (one page looked up
 // for 16 keys, where page_size is a multiple of 16, was no faster). A key that
 // is hidden or has no page is zero-filled and its score set to -inf, never
-// read, so what lies there cannot reach the result. Keys and values are read
-// once and marked to leave L2 first: parts, tables and what the next kernels
-// read stay there (without: 60.4 us for 58.6 on a batch of 16, 38.8 for 35.3
-// on one of 256 short sequences).
+// read, so what lies there cannot reach the result. Keys and values are marked
+// to leave L2 first: parts, tables and what the next kernels read stay there.
+// Without the mark a batch of 16 takes 60.6 us for 59.9, one of 256 short
+// sequences 38.8 for 36.0. Keys that are read again lose a little by it:
+// 16 sequences with 32768 keys in shared pages take 207 us for 200 without, 128
+// query heads on one K/V head (blocks of 16, each reading the keys) 70.0 for 68.3.
 //
 // Products (mma.sync m16n8k16, fp32 accumulators): S^T = K Q^T with the keys
 // as rows and 8 query heads as columns, then O^T += V^T P^T. The C fragment of
@@ -59,10 +61,13 @@
 // 54.3). lse takes the exact sum.
 //
 // Measured (device time, both kernels): one sequence of 131072 tokens, 8 K/V
-// heads, d 128 89 us (537 MB: 6.1 TB/s), 16 of 2048 to 8192 tokens 57.6 us
-// (336 MB: 5.8 TB/s), 256 of 20 to 300 tokens 35 us (171 MB: 4.9 TB/s), e4m3
-// 32 of 9 to 8192 tokens 54.7 us (269 MB: 4.9 TB/s; all 8192 long, head-major
-// pages, 91 us for 537 MB), 777 tokens 12 heads d 64 8.9 us. Of a long call 4
+// heads, d 128 89 us (537 MB: 6.1 TB/s), 16 of 2048 to 8192 tokens 57.5 us
+// (336 MB: 5.8 TB/s), 256 of 20 to 300 tokens 36 us (171 MB: 4.8 TB/s), e4m3
+// 32 of 9 to 8192 tokens 54.3 us (269 MB: 5.0 TB/s; all 8192 long, 89 us for 537
+// MB), 777 tokens 12 heads d 64 8.9 us. Beyond 16 heads a K/V head keys are read
+// again for every 16: 32 and 128 heads on one K/V head, 4 sequences of 32768
+// keys, 30 and 70 us where the bytes once want 10; d 256, 32 heads, 66 us (46
+// e4m3), where the 16-head kernels spill 76 to 252 bytes a thread. Of a long call 4
 // us pass before the first key arrives (lengths, page numbers, keys: three
 // trips to memory), and 5 to 9 between the first and the last SM's end: under
 // full load a fifth of the SMs get a tenth less bandwidth.
@@ -786,8 +791,8 @@ __global__ void __launch_bounds__(PdCfg<D, E, NT>::kThreads, 1)
 // one after another, the join took 8 us of the 95 of a 131072-key sequence;
 // so, 3 us); kAt = 1, rows side by side in a block, from kPdJoinUnits units on,
 // which have at most four parts on average (256 sequences of 20 to 300 tokens,
-// 8 K/V heads: 39 us in all, with kAt = 8 53; one sequence of 131072 tokens, 8
-// units: 93 and 90).
+// 8 K/V heads: 36 us in all, with kAt = 8 49; one sequence of 131072 tokens, 8
+// units: 89, with kAt = 1 91; 8 units of 16 heads, 32768 keys: 30 and 35).
 constexpr int kPdJoinUnits = 64;
 
 template <int D, int kAt>

@@ -16,16 +16,18 @@
 // token, keeps their A and B in registers and walks over the heads. In the
 // half layout they are the two chunks whose elements pair up (rotary_dim is a
 // multiple of 16, so whole chunks do), or two of those that are not turned;
-// interleaved, pairs stay in a chunk and any two do. No element crosses lanes then, and fp32
-// is multiplied in pairs (2 to 5 % faster than one by one). With one chunk a
-// thread, the partner's coming by shuffle and unpacked again, a chunk took 124
-// instructions where this takes 94. A row's d / 16 lanes lie in one warp, so
-// the sum of squares is a shuffle reduction.
+// interleaved, pairs stay in a chunk and any two do. No element crosses lanes
+// then, and fp32 is multiplied in pairs (2 to 5 % faster than one by one). With
+// one chunk a thread, the partner's coming by shuffle and unpacked again, a chunk
+// took 124 instructions where this takes 94. A row's d / 16 lanes lie in one
+// warp, so the sum of squares is a shuffle reduction.
 //
-// Angles: f_i / 2 pi, taken in fp64, becomes a 64-bit fixed-point fraction of a
-// turn, and its product with the position, modulo 2^64, is the angle's fraction
-// of a turn exactly (whole turns fall off the top): 2^-34 turns for any 32-bit
-// position, rounded to fp32 (2^-25 turns, 2e-7 rad) for sincospi. fp32
+// Angles: f_i / 2 pi, taken in fp64 (off by 2^-55 turns for f up to 1), becomes a
+// 64-bit fixed-point fraction of a turn, and its product with the position,
+// modulo 2^64, the angle's fraction of a turn; whole turns fall off the top and
+// the product adds no error. So the angle is off by the position times 2^-55
+// turns, 2^-24 at the last 32-bit position (2^-25.1 found for base 10000) and
+// within the rounding to fp32 for sincospi (2^-25 turns, 2e-7 rad) up to 2^30. fp32
 // products would be off by 0.01 rad at position 10^5. A block's angles are
 // computed once, cooperatively, into shared memory: a few sincospi a thread
 // for all its heads.

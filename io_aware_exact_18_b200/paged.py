@@ -71,7 +71,8 @@ def paged_append(k, v, k_cache, v_cache, block_table, positions, q=None, freqs=N
     seq[b] (int32 [B]; default b). Keys are normed and turned first as in
     :func:`qk_rotary` (norm_eps, k_weight, freqs; both None: stored as they
     come), and so is q [B, H, N, d] if given, into q_out (allocated unless
-    given; may be q). e4m3 pages hold value / descale, saturated. Tokens with a
+    given; may be q). e4m3 pages hold value / descale, saturated (descales above
+    2^-128). K and V pages must share no element. Tokens with a
     negative position are padding: nothing of them is written, and an allocated
     q_out holds arbitrary values in their rows. Tokens whose page the table does
     not give are dropped from the cache. Two tokens of a call must not go to the
