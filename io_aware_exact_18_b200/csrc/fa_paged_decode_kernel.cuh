@@ -52,13 +52,13 @@
 // the matrix pipe is idle most of the time, P enters the product as two bf16
 // parts (p rounded, and the rest rounded: 2^-16), which costs 0.5 % of the
 // time and leaves O with the rounding of its result alone; O is divided by the
-// exact sum. For e4m3 P is f16 (2^-11, a quarter of a bf16 result's own
+// exact sum. For e4m3 P is f16 (2^-11, an eighth of a bf16 result's own
 // rounding), and O is divided by the sum of the rounded probabilities. f16 ends
-// at 2^-24, so p is taken 2^7 larger there: a key that weighs 2^-32 of the
-// reference key still counts (at 2^-25 it did not before, and many such keys
-// were lost to O). A second f16 part takes 2 to 9 % longer (16 heads a K/V head,
-// 8 sequences of 16384 keys: 37.7 us for 34.5; the batch of 32 below 56.0 for
-// 54.3). lse takes the exact sum.
+// at 2^-24, so p is taken 2^7 larger there: keys above 2^-32 of the reference key
+// count, where many of them between that and 2^-25 would be lost to O. A second
+// f16 part takes 2 to 9 % longer (16 heads a K/V head, 8 sequences of 16384 keys:
+// 37.7 us for 34.5; the batch of 32 below 56.0 for 54.3). lse takes the exact
+// sum.
 //
 // Measured (device time, both kernels): one sequence of 131072 tokens, 8 K/V
 // heads, d 128 89 us (537 MB: 6.1 TB/s), 16 of 2048 to 8192 tokens 57.5 us
